@@ -40,10 +40,13 @@ __all__ = [
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libswiglu_mlp.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "swiglu_mlp.h")
+BLOCK_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "swiglu_block.h")
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+_INT = ctypes.c_int
+_F64 = ctypes.c_double
 
 _SIGNATURES = {
     "swiglu_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -78,6 +81,12 @@ _SIGNATURES = {
     "swiglu_moe_fwd": (ctypes.c_int, [_P] * 6 + [_P, _SZ] + [_I64] * 5 + [_P]),
     "swiglu_moe_bwd": (ctypes.c_int, [_P] * 9 + [_P, _SZ] + [_I64] * 5 + [_P]),
     "swiglu_moe_bwd_dgrad_fused": (ctypes.c_int, [_P] * 6 + [_I64] * 4 + [_P]),
+    # include/swiglu_block.h
+    "swiglu_block_abi_version": (ctypes.c_int, []),
+    "swiglu_layer_norm_fwd": (ctypes.c_int, [_P, _I64, _P, _P, _P, _I64, _P, _P, _I64, _I64, _F64, _INT, _INT, _P]),
+    "swiglu_layer_norm_bwd_workspace": (_SZ, [_I64] * 2),
+    "swiglu_layer_norm_bwd": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P, _P, _P, _SZ,
+                                             _I64, _I64, _INT, _INT, _P]),
 }
 
 
@@ -109,9 +118,11 @@ def lib() -> ctypes.CDLL:
 
 
 def exported_names():
-    """Function names declared in include/swiglu_mlp.h."""
-    with open(HEADER_PATH) as f:
-        text = f.read()
+    """Function names declared in include/swiglu_mlp.h and include/swiglu_block.h."""
+    text = ""
+    for path in (HEADER_PATH, BLOCK_HEADER_PATH):
+        with open(path) as f:
+            text += f.read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return sorted(set(re.findall(r"\b(swiglu_[a-z0-9_]+)\s*\(", text)))
 
@@ -125,15 +136,20 @@ def _check(fn: str, status: int):
         raise SwiGLUError(fn, status)
 
 
-def _on_device(t: torch.Tensor, name: str):
-    """t must be a contiguous tensor on the GPU the call launches on (the
-    current device inside a call, set from its first tensor)."""
+def _on_gpu(t: torch.Tensor, name: str):
+    """t must be a tensor on the GPU the call launches on (the current device
+    inside a call, set from its first tensor)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU (no CPU path)")
     if t.device.index != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{torch.cuda.current_device()}")
+
+
+def _on_device(t: torch.Tensor, name: str):
+    """_on_gpu, and contiguous."""
+    _on_gpu(t, name)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous (row-major)")
 
@@ -175,6 +191,10 @@ def _launches(fn):
         if not isinstance(like, torch.Tensor) or not like.is_cuda:
             raise ValueError(f"{fn.__name__}: the first argument must be a tensor on a GPU (no CPU path)")
         stream = kw.get("stream")
+        if stream is None and like.device.index == torch.cuda.current_device():
+            # the device and its stream are current already
+            kw["stream"] = torch.cuda.current_stream()
+            return fn(*args, **kw)
         if stream is None:
             st = torch.cuda.current_stream(like.device)
         elif isinstance(stream, torch.cuda.Stream):
@@ -680,3 +700,9 @@ class SwiGLUMoEFunction(torch.autograd.Function):
 
 def swiglu_moe(x, W1, W_down, group_offsets):
     return SwiGLUMoEFunction.apply(x, W1, W_down, group_offsets)
+
+
+from . import block as _block  # noqa: E402  (uses the helpers above)
+from .block import *  # noqa: E402,F401,F403
+
+__all__ += _block.__all__

@@ -6,10 +6,12 @@ environment variable ``SWIGLU_HIPCC_FLAGS`` (diagnostics only).
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import shlex
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,7 +24,6 @@ FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     # identical fp32 rounding in every kernel that computes h: no implicit
     # contraction of a*b+c into fma (explicit fmaf only)
     "-ffp-contract=off",
@@ -32,11 +33,11 @@ FLAGS = [
 ]
 
 
-def build(verbose: bool = False) -> str:
-    src = os.path.join(CSRC, "swiglu_mlp.hip")
-    tmp = LIB + ".tmp"
-    cmd = [HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC, src, "-o", tmp]
-    cmd += shlex.split(os.environ.get("SWIGLU_HIPCC_FLAGS", ""))
+SOURCES = ["swiglu_mlp.hip", "layer_norm.hip"]
+
+
+def _hipcc(args, verbose: bool) -> None:
+    cmd = [HIPCC, *FLAGS, *args]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -47,7 +48,19 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError("hipcc failed:\n" + "\n".join(lines))
     if verbose and lines:
         print("\n".join(lines))
-    os.replace(tmp, LIB)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile every source (in parallel) and link them into one library."""
+    extra = shlex.split(os.environ.get("SWIGLU_HIPCC_FLAGS", ""))
+    with tempfile.TemporaryDirectory() as tmp, concurrent.futures.ThreadPoolExecutor() as pool:
+        objs = [os.path.join(tmp, s + ".o") for s in SOURCES]
+        jobs = [pool.submit(_hipcc, ["-c", "-I", os.path.join(ROOT, "include"), "-I", CSRC, os.path.join(CSRC, s),
+                                     "-o", o, *extra], verbose) for s, o in zip(SOURCES, objs)]
+        for j in jobs:
+            j.result()
+        _hipcc(["-shared", *objs, "-o", LIB + ".tmp", *extra], verbose)
+    os.replace(LIB + ".tmp", LIB)
     return LIB
 
 

@@ -1,0 +1,109 @@
+// block_common.hpp -- what the operators around the MLP step share: element
+// types, 16-byte vectors of any element alignment, wave sums, and the host's
+// argument checks.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "swiglu_block.h"
+
+#define SW_TRY(expr)                  \
+  do {                                \
+    int _s = (expr);                  \
+    if (_s != SWIGLU_OK) return _s;   \
+  } while (0)
+
+namespace swb {
+
+// ---- element types ---------------------------------------------------------
+typedef __bf16 bf16_t;
+typedef _Float16 fp16_t;
+
+// VEC elements in 16 bytes.  The vector type is declared with the alignment
+// of one element: gfx950 serves a 16-byte global access at any dword (and, in
+// the unaligned mode that the ROCm runtime sets, any byte) address, so rows of
+// an odd width and views that start anywhere take the same wide loads.
+template <class T>
+struct Vec {
+  static constexpr int N = 16 / (int)sizeof(T);
+  typedef T type __attribute__((ext_vector_type(16 / sizeof(T))));
+  typedef type loose __attribute__((aligned(sizeof(T))));
+};
+template <class T>
+__device__ __forceinline__ typename Vec<T>::type load_vec(const T* p) {
+  return *(const typename Vec<T>::loose*)p;
+}
+template <class T>
+__device__ __forceinline__ void store_vec(T* p, typename Vec<T>::type v) {
+  *(typename Vec<T>::loose*)p = v;
+}
+// N values of type W as floats, N a multiple of W's vector
+template <int N, class W>
+__device__ __forceinline__ void load_floats(const W* p, float (&f)[N]) {
+  constexpr int V = Vec<W>::N;
+  if constexpr (N >= V) {
+#pragma unroll
+    for (int i = 0; i < N / V; ++i) {
+      const auto v = load_vec<W>(p + i * V);
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[i * V + e] = (float)v[e];
+    }
+  } else {
+    // four 16-bit weights beside a vector of four floats
+    typedef W part __attribute__((ext_vector_type(N)));
+    typedef part loose __attribute__((aligned(sizeof(W))));
+    const part v = *(const loose*)p;
+#pragma unroll
+    for (int e = 0; e < N; ++e) f[e] = (float)v[e];
+  }
+}
+
+// ---- wave sums ---------------------------------------------------------------
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false);
+  return v + __builtin_bit_cast(float, o);
+}
+// The sum over the 64 lanes, the same value in every lane.  All lanes active.
+// Four steps inside rows of 16 lanes (register-to-register, no LDS), then the
+// four rows by reading one lane of each.
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_add<0xB1>(v);   // quad_perm 1,0,3,2
+  v = dpp_add<0x4E>(v);   // quad_perm 2,3,0,1
+  v = dpp_add<0x141>(v);  // mirror within 8 lanes
+  v = dpp_add<0x140>(v);  // mirror within 16 lanes
+  const int b = __builtin_bit_cast(int, v);
+  const float r0 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 0));
+  const float r1 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 16));
+  const float r2 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 32));
+  const float r3 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 48));
+  return (r0 + r1) + (r2 + r3);
+}
+
+// ---- host side -----------------------------------------------------------------
+struct Range {
+  uintptr_t lo, hi;
+};
+inline Range rng(const void* p, int64_t bytes) {
+  return Range{(uintptr_t)p, (uintptr_t)p + (uintptr_t)(p ? bytes : 0)};
+}
+inline bool overlap(const Range& a, const Range& b) {
+  return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo;
+}
+inline int check_alias(const Range* ins, int n_in, const Range* outs, int n_out) {
+  for (int o = 0; o < n_out; ++o) {
+    for (int i = 0; i < n_in; ++i)
+      if (overlap(outs[o], ins[i])) return SWIGLU_ERR_ALIAS;
+    for (int j = o + 1; j < n_out; ++j)
+      if (overlap(outs[o], outs[j])) return SWIGLU_ERR_ALIAS;
+  }
+  return SWIGLU_OK;
+}
+inline bool aligned_to(const void* p, int n) { return ((uintptr_t)p & (uintptr_t)(n - 1)) == 0; }
+inline size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
+inline int elem_size(int dtype) { return dtype == SWIGLU_FP32 ? 4 : 2; }
+inline bool dtype_ok(int dtype) { return dtype == SWIGLU_BF16 || dtype == SWIGLU_FP16 || dtype == SWIGLU_FP32; }
+inline int launch_status() { return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_HIP; }
+inline hipStream_t as_stream(void* s) { return (hipStream_t)s; }
+
+}  // namespace swb

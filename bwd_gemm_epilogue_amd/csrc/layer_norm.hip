@@ -1,0 +1,632 @@
+// layer_norm.hip -- layer norm forward and backward on gfx950, with the
+// reduction of the weight's and the bias's gradient.
+//
+// Forward, per row: mean, then the centred second moment from the row held in
+// registers (a second pass over registers, so a large mean costs no digits),
+// then y = (x - mean) rstd w + b.  Backward, per row, with xh = (x - mean)
+// rstd and g = dy w:
+//   dx = rstd (g - sum(g)/D - xh sum(g xh)/D) (+ dres)
+// and, over all rows, dw = sum dy xh, db = sum dy.
+//
+// Both are bound by HBM: every element is read once into registers and written
+// once.  A row belongs to one wave (64 lanes) while a lane's share of it fits
+// its registers, so that the forward and the row part of the backward need
+// neither LDS nor a barrier; wider rows go to a workgroup.
+#include "block_common.hpp"
+
+namespace swb {
+
+// sum over the G threads of a row (G = 64: a wave; G = 256: the workgroup,
+// through `red`, two floats per wave and call; the two barriers of
+// the caller's next call keep a slow reader apart from the next writer)
+template <int G>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = wave_sum(v);
+  if constexpr (G == 256) {
+    const int w = threadIdx.x >> 6;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[w] = v;
+    __syncthreads();
+    v = (red[0] + red[1]) + (red[2] + red[3]);
+  }
+  return v;
+}
+template <int G>
+__device__ __forceinline__ void row_sum2(float& a, float& b, float* red) {
+  a = wave_sum(a);
+  b = wave_sum(b);
+  if constexpr (G == 256) {
+    const int w = threadIdx.x >> 6;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) {
+      red[w] = a;
+      red[4 + w] = b;
+    }
+    __syncthreads();
+    a = (red[0] + red[1]) + (red[2] + red[3]);
+    b = (red[4] + red[5]) + (red[6] + red[7]);
+  }
+}
+
+struct FwdArgs {
+  const void *x, *w, *b;
+  void* y;
+  float *mean, *rstd;
+  int64_t ldx, ldy, M;
+  int D;
+  float inv_d;
+  double eps;
+};
+
+// 1 / sqrt(v): the hardware's reciprocal square root, one Newton step to round
+// it as well as a division would
+__device__ __forceinline__ float rstd_of(float var, float eps) {
+  const float a = var + eps;
+  float r = __builtin_amdgcn_rsqf(a);
+  const float e = __builtin_fmaf(-a * r, r, 1.0f);
+  // a = 0 or inf: r is inf or 0 and stays
+  return (a > 0.0f && a < __builtin_inff()) ? __builtin_fmaf(0.5f * r, e, r) : r;
+}
+
+// One row to G threads, NV 16-byte vectors of it to a thread, and the D % VEC
+// last elements one to each of the first threads.
+template <class T, class W, int G, int NV>
+__global__ void __launch_bounds__(256) ln_fwd_kernel(const FwdArgs a) {
+  constexpr int VEC = Vec<T>::N;
+  __shared__ float red[8];
+  const int tl = threadIdx.x & (G - 1);
+  int64_t row = blockIdx.x;
+  if constexpr (G == 64) row = row * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (row >= a.M) return;  // a wave's (G = 64: no barrier follows) or the whole workgroup's
+  const int D = a.D, nvec = D / VEC, tail = nvec * VEC + tl;
+  const T* x = (const T*)a.x + row * a.ldx;
+  typename Vec<T>::type r[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = tl + i * G;
+    if (v < nvec) r[i] = load_vec(x + v * VEC);
+  }
+  const float xt = tail < D ? (float)x[tail] : 0.0f;
+  float s = xt;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (tl + i * G < nvec) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s += (float)r[i][e];
+    }
+  }
+  const float mean = row_sum<G>(s, red) * a.inv_d;
+  float q = tail < D ? (xt - mean) * (xt - mean) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (tl + i * G < nvec) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float c = (float)r[i][e] - mean;
+        q = __builtin_fmaf(c, c, q);
+      }
+    }
+  }
+  const float rstd = rstd_of(row_sum<G>(q, red) * a.inv_d, (float)a.eps);
+  if (tl == 0) {
+    if (a.mean) a.mean[row] = mean;
+    if (a.rstd) a.rstd[row] = rstd;
+  }
+  T* y = (T*)a.y + row * a.ldy;
+  const W *w = (const W*)a.w, *b = (const W*)a.b;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = tl + i * G;
+    if (v < nvec) {
+      float wf[VEC], bf[VEC];
+      if (w) load_floats<VEC>(w + v * VEC, wf);
+      if (b) load_floats<VEC>(b + v * VEC, bf);
+      typename Vec<T>::type o;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        float u = ((float)r[i][e] - mean) * rstd;
+        if (w) u *= wf[e];
+        if (b) u += bf[e];
+        o[e] = (T)u;
+      }
+      store_vec(y + v * VEC, o);
+    }
+  }
+  if (tail < D) {
+    float u = (xt - mean) * rstd;
+    if (w) u *= (float)w[tail];
+    if (b) u += (float)b[tail];
+    y[tail] = (T)u;
+  }
+}
+
+// A row that does not fit the registers of a workgroup: three passes, the
+// second and third from the cache (a row is at most 4 MB).
+template <class T, class W>
+__global__ void __launch_bounds__(256) ln_fwd_wide_kernel(const FwdArgs a) {
+  __shared__ float red[8];
+  const int64_t row = blockIdx.x;
+  const T* x = (const T*)a.x + row * a.ldx;
+  T* y = (T*)a.y + row * a.ldy;
+  const W *w = (const W*)a.w, *b = (const W*)a.b;
+  constexpr int VEC = Vec<T>::N;
+  const int D = a.D, nvec = D / VEC, tail = nvec * VEC + (int)threadIdx.x;
+  float s = tail < D ? (float)x[tail] : 0.0f;
+  for (int v = threadIdx.x; v < nvec; v += 256) {
+    const auto r = load_vec(x + (int64_t)v * VEC);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) s += (float)r[e];
+  }
+  const float mean = row_sum<256>(s, red) * a.inv_d;
+  float q = 0.0f;
+  if (tail < D) q = ((float)x[tail] - mean) * ((float)x[tail] - mean);
+  for (int v = threadIdx.x; v < nvec; v += 256) {
+    const auto r = load_vec(x + (int64_t)v * VEC);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float c = (float)r[e] - mean;
+      q = __builtin_fmaf(c, c, q);
+    }
+  }
+  const float rstd = rstd_of(row_sum<256>(q, red) * a.inv_d, (float)a.eps);
+  if (threadIdx.x == 0) {
+    if (a.mean) a.mean[row] = mean;
+    if (a.rstd) a.rstd[row] = rstd;
+  }
+  for (int v = threadIdx.x; v < nvec; v += 256) {
+    const auto r = load_vec(x + (int64_t)v * VEC);
+    typename Vec<T>::type o;
+    float wf[VEC], bf[VEC];
+    if (w) load_floats<VEC>(w + v * VEC, wf);
+    if (b) load_floats<VEC>(b + v * VEC, bf);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      float u = ((float)r[e] - mean) * rstd;
+      if (w) u *= wf[e];
+      if (b) u += bf[e];
+      o[e] = (T)u;
+    }
+    store_vec(y + (int64_t)v * VEC, o);
+  }
+  if (tail < D) {
+    float u = ((float)x[tail] - mean) * rstd;
+    if (w) u *= (float)w[tail];
+    if (b) u += (float)b[tail];
+    y[tail] = (T)u;
+  }
+}
+
+struct BwdArgs {
+  const void *dy, *x, *w, *dres;
+  const float *mean, *rstd;
+  void* dx;
+  float* part;  // [gridDim.x][want_b ? 2 : 1][D]: dw, then db (NULL: neither is wanted)
+  int64_t lddy, ldx, lddres, lddx, M;
+  int D;
+  int want_b;
+  float inv_d;
+};
+
+// A workgroup walks rows r, r + gridDim*ROWS, ..., ROWS = THREADS/G at a time,
+// and keeps its columns' sums of dy xh and dy in registers; at the end its
+// waves' sums are added through LDS and written once.
+template <class T, class W, int G, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS) ln_bwd_kernel(const BwdArgs a) {
+  constexpr int VEC = Vec<T>::N, ROWS = THREADS / G, C = NV * VEC;
+  static_assert(G == 64 || ROWS == 1, "a row is a wave's or the workgroup's");
+  __shared__ float red[8];
+  // ROWS > 1: [ROWS/2][2][C][G] sums of the columns, then [ROWS/2][2][G] of the tail
+  __shared__ float acc_lds[ROWS > 1 ? ROWS / 2 * 2 * (C + 1) * G : 1];
+  const int tl = threadIdx.x & (G - 1);
+  const int sub = G == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  const int D = a.D, nvec = D / VEC, tail = nvec * VEC + tl;
+  const W* w = (const W*)a.w;
+  float dw[C], db[C], dwt = 0.0f, dbt = 0.0f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) dw[c] = db[c] = 0.0f;
+  const float wt = tail < D ? (w ? (float)w[tail] : 1.0f) : 0.0f;
+  for (int64_t row = (int64_t)blockIdx.x * ROWS + sub; row < a.M; row += (int64_t)gridDim.x * ROWS) {
+    const T* x = (const T*)a.x + row * a.ldx;
+    const T* dy = (const T*)a.dy + row * a.lddy;
+    const T* rs = (const T*)a.dres + row * a.lddres;
+    T* dx = (T*)a.dx + row * a.lddx;
+    typename Vec<T>::type xr[NV], yr[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = tl + i * G;
+      if (v < nvec) {
+        xr[i] = load_vec(x + v * VEC);
+        yr[i] = load_vec(dy + v * VEC);
+      }
+    }
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    const float dyt = tail < D ? (float)dy[tail] : 0.0f;
+    const float xht = tail < D ? ((float)x[tail] - mean) * rstd : 0.0f;
+    dwt = __builtin_fmaf(dyt, xht, dwt);
+    dbt += dyt;
+    float s1 = dyt * wt, s2 = dyt * wt * xht;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = tl + i * G;
+      if (v < nvec) {
+        float wf[VEC];
+        if (w) load_floats<VEC>(w + v * VEC, wf);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float d = (float)yr[i][e], xh = ((float)xr[i][e] - mean) * rstd;
+          const float g = w ? d * wf[e] : d;
+          dw[i * VEC + e] = __builtin_fmaf(d, xh, dw[i * VEC + e]);
+          db[i * VEC + e] += d;
+          s1 += g;
+          s2 = __builtin_fmaf(g, xh, s2);
+        }
+      }
+    }
+    row_sum2<G>(s1, s2, red);
+    const float m1 = s1 * a.inv_d, m2 = s2 * a.inv_d;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = tl + i * G;
+      if (v < nvec) {
+        float wf[VEC];
+        if (w) load_floats<VEC>(w + v * VEC, wf);
+        typename Vec<T>::type rr, o;
+        if (a.dres) rr = load_vec(rs + v * VEC);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float d = (float)yr[i][e], xh = ((float)xr[i][e] - mean) * rstd;
+          const float g = w ? d * wf[e] : d;
+          float u = (__builtin_fmaf(-xh, m2, g - m1)) * rstd;
+          if (a.dres) u += (float)rr[e];
+          o[e] = (T)u;
+        }
+        store_vec(dx + v * VEC, o);
+      }
+    }
+    if (tail < D) {
+      float u = (dyt * wt - m1 - xht * m2) * rstd;
+      if (a.dres) u += (float)rs[tail];
+      dx[tail] = (T)u;
+    }
+  }
+  if (!a.part) return;
+  // Pairs of rows added through LDS until one wave holds the workgroup's sums
+  if constexpr (ROWS > 1) {
+    float* tl_lds = acc_lds + ROWS / 2 * 2 * C * G;
+#pragma unroll
+    for (int half = ROWS / 2; half >= 1; half >>= 1) {
+      if (sub >= half && sub < 2 * half) {
+        float* p = acc_lds + (sub - half) * 2 * C * G + tl;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          p[c * G] = dw[c];
+          p[(C + c) * G] = db[c];
+        }
+        tl_lds[(sub - half) * 2 * G + tl] = dwt;
+        tl_lds[(sub - half) * 2 * G + G + tl] = dbt;
+      }
+      __syncthreads();
+      if (sub < half) {
+        const float* p = acc_lds + sub * 2 * C * G + tl;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          dw[c] += p[c * G];
+          db[c] += p[(C + c) * G];
+        }
+        dwt += tl_lds[sub * 2 * G + tl];
+        dbt += tl_lds[sub * 2 * G + G + tl];
+      }
+      __syncthreads();
+    }
+  }
+  if (sub == 0) {
+    float* p = a.part + (int64_t)blockIdx.x * (a.want_b ? 2 : 1) * D;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = tl + i * G;
+      if (v < nvec) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) p[v * VEC + e] = dw[i * VEC + e];
+        if (a.want_b) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) p[D + v * VEC + e] = db[i * VEC + e];
+        }
+      }
+    }
+    if (tail < D) {
+      p[tail] = dwt;
+      if (a.want_b) p[D + tail] = dbt;
+    }
+  }
+}
+
+// dx of a row that does not fit the registers of a workgroup
+template <class T, class W>
+__global__ void __launch_bounds__(256) ln_bwd_wide_kernel(const BwdArgs a) {
+  constexpr int VEC = Vec<T>::N;
+  __shared__ float red[8];
+  const int64_t row = blockIdx.x;
+  const T* x = (const T*)a.x + row * a.ldx;
+  const T* dy = (const T*)a.dy + row * a.lddy;
+  const T* rs = (const T*)a.dres + row * a.lddres;
+  T* dx = (T*)a.dx + row * a.lddx;
+  const W* w = (const W*)a.w;
+  const int D = a.D, nvec = D / VEC, tail = nvec * VEC + (int)threadIdx.x;
+  const float mean = a.mean[row], rstd = a.rstd[row];
+  float s1 = 0.0f, s2 = 0.0f, gt = 0.0f, xht = 0.0f;
+  if (tail < D) {
+    gt = (float)dy[tail] * (w ? (float)w[tail] : 1.0f);
+    xht = ((float)x[tail] - mean) * rstd;
+    s1 = gt;
+    s2 = gt * xht;
+  }
+  for (int v = threadIdx.x; v < nvec; v += 256) {
+    const auto xr = load_vec(x + (int64_t)v * VEC);
+    const auto yr = load_vec(dy + (int64_t)v * VEC);
+    float wf[VEC];
+    if (w) load_floats<VEC>(w + v * VEC, wf);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float g = w ? (float)yr[e] * wf[e] : (float)yr[e];
+      s1 += g;
+      s2 = __builtin_fmaf(g, ((float)xr[e] - mean) * rstd, s2);
+    }
+  }
+  row_sum2<256>(s1, s2, red);
+  const float m1 = s1 * a.inv_d, m2 = s2 * a.inv_d;
+  for (int v = threadIdx.x; v < nvec; v += 256) {
+    const auto xr = load_vec(x + (int64_t)v * VEC);
+    const auto yr = load_vec(dy + (int64_t)v * VEC);
+    typename Vec<T>::type rr, o;
+    if (a.dres) rr = load_vec(rs + (int64_t)v * VEC);
+    float wf[VEC];
+    if (w) load_floats<VEC>(w + v * VEC, wf);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float g = w ? (float)yr[e] * wf[e] : (float)yr[e];
+      float u = __builtin_fmaf(-((float)xr[e] - mean) * rstd, m2, g - m1) * rstd;
+      if (a.dres) u += (float)rr[e];
+      o[e] = (T)u;
+    }
+    store_vec(dx + (int64_t)v * VEC, o);
+  }
+  if (tail < D) {
+    float u = (gt - m1 - xht * m2) * rstd;
+    if (a.dres) u += (float)rs[tail];
+    dx[tail] = (T)u;
+  }
+}
+
+// The wide rows' dw and db: a workgroup sums 256 columns over one slice of the
+// rows, blockIdx.y of gridDim.y, into that slice's partial sums.
+template <class T>
+__global__ void __launch_bounds__(256) ln_bwd_wide_cols_kernel(const BwdArgs a) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= a.D) return;
+  const int64_t r0 = a.M * blockIdx.y / gridDim.y, r1 = a.M * (blockIdx.y + 1) / gridDim.y;
+  float dw = 0.0f, db = 0.0f;
+  for (int64_t row = r0; row < r1; ++row) {
+    const float d = (float)((const T*)a.dy)[row * a.lddy + c];
+    const float xh = ((float)((const T*)a.x)[row * a.ldx + c] - a.mean[row]) * a.rstd[row];
+    dw = __builtin_fmaf(d, xh, dw);
+    db += d;
+  }
+  float* p = a.part + (int64_t)blockIdx.y * (a.want_b ? 2 : 1) * a.D;
+  p[c] = dw;
+  if (a.want_b) p[a.D + c] = db;
+}
+
+// dw[c] (and db[c] = column D + c) = the parts' sum, in order.  A workgroup
+// takes 64 columns; its four waves take a quarter of the parts each.
+template <class W>
+__global__ void __launch_bounds__(256) ln_bwd_cols_kernel(const float* __restrict__ part, int parts, int D, int cols,
+                                                          W* __restrict__ dw, W* __restrict__ db) {
+  __shared__ float red[4][64];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
+  const int p0 = parts * wv / 4, p1 = parts * (wv + 1) / 4;
+  float s = 0.0f;
+  if (c < cols) {
+    int p = p0;
+    for (; p + 8 <= p1; p += 8) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = part[(int64_t)(p + u) * cols + c];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += v[u];
+    }
+    for (; p < p1; ++p) s += part[(int64_t)p * cols + c];
+  }
+  red[wv][lane] = s;
+  __syncthreads();
+  if (wv == 0 && c < cols) {
+    const float t = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+    if (c < D) {
+      if (dw) dw[c] = (W)t;
+    } else {
+      db[c - D] = (W)t;
+    }
+  }
+}
+
+}  // namespace swb
+
+// ===========================================================================
+// Host side
+// ===========================================================================
+namespace {
+
+using namespace swb;
+
+constexpr int64_t kMaxNormDim = (int64_t)1 << 20;
+// Elements of a row that one wave (64 lanes of 64 elements) and one workgroup
+// (256 threads of 64) keep in registers.
+constexpr int64_t kWaveRow = 64 * 64, kGroupRow = 256 * 64;
+constexpr int kBwdThreads = 512;   // G = 64: eight waves, eight rows at a time
+constexpr int64_t kBwdGroups = 256;  // workgroups of the row pass, and parts of dw and db
+
+template <class T, class W, int G, int NV>
+int fwd_go(const FwdArgs& a, hipStream_t st) {
+  const int64_t per = 256 / G, blocks = (a.M + per - 1) / per;
+  hipLaunchKernelGGL((ln_fwd_kernel<T, W, G, NV>), dim3((unsigned)blocks), dim3(256), 0, st, a);
+  return launch_status();
+}
+
+template <class T, class W>
+int fwd_typed(const FwdArgs& a, hipStream_t st) {
+  constexpr int V = Vec<T>::N;
+  if (a.D <= 64 * 8) return fwd_go<T, W, 64, 8 / V>(a, st);
+  if (a.D <= 64 * 16) return fwd_go<T, W, 64, 16 / V>(a, st);
+  if (a.D <= 64 * 32) return fwd_go<T, W, 64, 32 / V>(a, st);
+  if (a.D <= kWaveRow) return fwd_go<T, W, 64, 64 / V>(a, st);
+  if (a.D <= 256 * 32) return fwd_go<T, W, 256, 32 / V>(a, st);
+  if (a.D <= kGroupRow) return fwd_go<T, W, 256, 64 / V>(a, st);
+  hipLaunchKernelGGL((ln_fwd_wide_kernel<T, W>), dim3((unsigned)a.M), dim3(256), 0, st, a);
+  return launch_status();
+}
+
+template <class T, class W, int G, int NV>
+int bwd_rows(const BwdArgs& a, int64_t parts, hipStream_t st) {
+  constexpr int THREADS = G == 64 ? kBwdThreads : G;
+  hipLaunchKernelGGL((ln_bwd_kernel<T, W, G, NV, THREADS>), dim3((unsigned)parts), dim3(THREADS), 0, st, a);
+  return launch_status();
+}
+
+template <class T, class W>
+int bwd_typed(const BwdArgs& a, void* dw, void* db, hipStream_t st) {
+  constexpr int V = Vec<T>::N;
+  constexpr int64_t wave_row = sizeof(T) == 2 ? kWaveRow : kWaveRow / 2;
+  // workgroups of the row pass, each with one part of dw and db
+  const int64_t rows = a.D <= wave_row ? kBwdThreads / 64 : 1;
+  const int64_t parts = (a.M + rows - 1) / rows < kBwdGroups ? (a.M + rows - 1) / rows : kBwdGroups;
+  int s;
+  if (a.D <= 64 * 8) s = bwd_rows<T, W, 64, 8 / V>(a, parts, st);
+  else if (a.D <= 64 * 16) s = bwd_rows<T, W, 64, 16 / V>(a, parts, st);
+  else if (a.D <= 64 * 32) s = bwd_rows<T, W, 64, 32 / V>(a, parts, st);
+  else if (a.D <= wave_row) s = bwd_rows<T, W, 64, (sizeof(T) == 2 ? 64 : 32) / V>(a, parts, st);
+  else if (a.D <= 256 * 32) s = bwd_rows<T, W, 256, 32 / V>(a, parts, st);
+  else if (a.D <= kGroupRow) s = bwd_rows<T, W, 256, 64 / V>(a, parts, st);
+  else {
+    hipLaunchKernelGGL((ln_bwd_wide_kernel<T, W>), dim3((unsigned)a.M), dim3(256), 0, st, a);
+    s = launch_status();
+    if (s == SWIGLU_OK && a.part) {
+      hipLaunchKernelGGL((ln_bwd_wide_cols_kernel<T>), dim3((unsigned)((a.D + 255) / 256), (unsigned)parts), dim3(256),
+                         0, st, a);
+      s = launch_status();
+    }
+  }
+  if (s != SWIGLU_OK || !a.part) return s;
+  const int cols = a.want_b ? 2 * a.D : a.D;
+  hipLaunchKernelGGL((ln_bwd_cols_kernel<W>), dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, st,
+                     (const float*)a.part, (int)parts, a.D, cols, (W*)dw, (W*)db);
+  return launch_status();
+}
+
+__global__ void __launch_bounds__(256) zero_bytes_kernel(uint16_t* p, int64_t n) {
+  for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < n; t += (int64_t)gridDim.x * blockDim.x)
+    p[t] = 0;
+}
+int zero_fill(void* p, int64_t bytes, hipStream_t st) {
+  const int64_t n = bytes / 2;
+  hipLaunchKernelGGL(zero_bytes_kernel, dim3((unsigned)((n + 255) / 256 < 1024 ? (n + 255) / 256 : 1024)), dim3(256), 0,
+                     st, (uint16_t*)p, n);
+  return launch_status();
+}
+
+int check_norm_shape(int64_t M, int64_t D) {
+  if (M < 0 || D <= 0) return SWIGLU_ERR_SHAPE;
+  if (M > ((int64_t)1 << 31) - 1 || D > kMaxNormDim) return SWIGLU_ERR_UNSUPPORTED;
+  return SWIGLU_OK;
+}
+int check_norm_types(int dtype, int wdtype) {
+  if (!dtype_ok(dtype) || !dtype_ok(wdtype)) return SWIGLU_ERR_UNSUPPORTED;
+  return wdtype == dtype || wdtype == SWIGLU_FP32 ? SWIGLU_OK : SWIGLU_ERR_UNSUPPORTED;
+}
+// a row stride that holds a row, and a tensor that stays addressable
+int check_ld(int64_t ld, int64_t D) {
+  if (ld < D) return SWIGLU_ERR_SHAPE;
+  return ld > ((int64_t)1 << 31) ? SWIGLU_ERR_UNSUPPORTED : SWIGLU_OK;
+}
+Range rows_range(const void* p, int64_t M, int64_t ld, int64_t D, int es) {
+  return rng(p, M > 0 ? ((M - 1) * ld + D) * es : 0);
+}
+
+template <class F>
+int by_type(int dtype, int wdtype, F&& f) {
+  if (dtype == SWIGLU_BF16) return wdtype == SWIGLU_BF16 ? f(bf16_t{}, bf16_t{}) : f(bf16_t{}, float{});
+  if (dtype == SWIGLU_FP16) return wdtype == SWIGLU_FP16 ? f(fp16_t{}, fp16_t{}) : f(fp16_t{}, float{});
+  return f(float{}, float{});
+}
+
+}  // namespace
+
+extern "C" {
+
+int swiglu_block_abi_version(void) { return (1 << 16) | 0; }
+
+int swiglu_layer_norm_fwd(const void* x, int64_t ldx, const void* weight, const void* bias, void* y, int64_t ldy,
+                          float* mean, float* rstd, int64_t M, int64_t D, double eps, int dtype, int wdtype,
+                          void* stream) {
+  SW_TRY(check_norm_shape(M, D));
+  SW_TRY(check_norm_types(dtype, wdtype));
+  SW_TRY(check_ld(ldx, D));
+  SW_TRY(check_ld(ldy, D));
+  if (!(eps >= 0.0)) return SWIGLU_ERR_SHAPE;
+  if (M > 0 && (!x || !y)) return SWIGLU_ERR_NULL;
+  const int es = elem_size(dtype), ws = elem_size(wdtype);
+  if (!aligned_to(x, es) || !aligned_to(y, es) || !aligned_to(weight, ws) || !aligned_to(bias, ws) ||
+      !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+    return SWIGLU_ERR_ALIGN;
+  const Range ins[] = {rows_range(x, M, ldx, D, es), rng(weight, D * ws), rng(bias, D * ws)};
+  const Range outs[] = {rows_range(y, M, ldy, D, es), rng(mean, M * 4), rng(rstd, M * 4)};
+  SW_TRY(check_alias(ins, 3, outs, 3));
+  if (M == 0) return SWIGLU_OK;
+  const FwdArgs a{x, weight, bias, y, mean, rstd, ldx, ldy, M, (int)D, (float)(1.0 / (double)D), eps};
+  return by_type(dtype, wdtype, [&](auto t, auto w) { return fwd_typed<decltype(t), decltype(w)>(a, as_stream(stream)); });
+}
+
+size_t swiglu_layer_norm_bwd_workspace(int64_t M, int64_t D) {
+  if (check_norm_shape(M, D) != SWIGLU_OK) return 0;
+  // at most one part for each row
+  return align256((size_t)((M < kBwdGroups ? M : kBwdGroups) * 2 * D * 4));
+}
+
+int swiglu_layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* weight,
+                          const float* mean, const float* rstd, const void* dres, int64_t lddres, void* dx,
+                          int64_t lddx, void* dweight, void* dbias, void* ws, size_t ws_bytes, int64_t M, int64_t D,
+                          int dtype, int wdtype, void* stream) {
+  SW_TRY(check_norm_shape(M, D));
+  SW_TRY(check_norm_types(dtype, wdtype));
+  SW_TRY(check_ld(lddy, D));
+  SW_TRY(check_ld(ldx, D));
+  if (dres) SW_TRY(check_ld(lddres, D));
+  SW_TRY(check_ld(lddx, D));
+  if (M > 0 && (!dy || !x || !mean || !rstd || !dx)) return SWIGLU_ERR_NULL;
+  const int es = elem_size(dtype), wsz = elem_size(wdtype);
+  if (!aligned_to(dy, es) || !aligned_to(x, es) || !aligned_to(dres, es) || !aligned_to(dx, es) ||
+      !aligned_to(weight, wsz) || !aligned_to(dweight, wsz) || !aligned_to(dbias, wsz) || !aligned_to(mean, 4) ||
+      !aligned_to(rstd, 4) || !aligned_to(ws, 16))
+    return SWIGLU_ERR_ALIGN;
+  const bool want = dweight || dbias;
+  const size_t need = want ? swiglu_layer_norm_bwd_workspace(M, D) : 0;
+  if (need > 0 && (!ws || ws_bytes < need)) return SWIGLU_ERR_WORKSPACE;
+  const Range ins[] = {rows_range(dy, M, lddy, D, es), rows_range(x, M, ldx, D, es),
+                       rng(weight, D * wsz),           rng(mean, M * 4),
+                       rng(rstd, M * 4),               rows_range(dres, M, lddres, D, es)};
+  const Range outs[] = {rows_range(dx, M, lddx, D, es), rng(dweight, D * wsz), rng(dbias, D * wsz),
+                        rng(ws, (int64_t)need)};
+  SW_TRY(check_alias(ins, 6, outs, 4));
+  hipStream_t st = as_stream(stream);
+  if (M == 0) {
+    if (dweight) SW_TRY(zero_fill(dweight, D * wsz, st));
+    if (dbias) SW_TRY(zero_fill(dbias, D * wsz, st));
+    return SWIGLU_OK;
+  }
+  const BwdArgs a{dy,   x,   weight, dres,   mean, rstd,   dx, want ? (float*)ws : nullptr,
+                  lddy, ldx, lddres, lddx,   M,    (int)D, dbias ? 1 : 0,
+                  (float)(1.0 / (double)D)};
+  return by_type(dtype, wdtype,
+                 [&](auto t, auto w) { return bwd_typed<decltype(t), decltype(w)>(a, dweight, dbias, st); });
+}
+
+}  // extern "C"

@@ -1,0 +1,67 @@
+/*
+ * swiglu_block.h -- C ABI of the operators around the SwiGLU MLP step
+ * (swiglu_mlp.h) in a block that trains or serves it, on MI355X (gfx950):
+ *   - layer norm, forward and backward (in front of the MLP).
+ *
+ * Conventions, where they are not those of swiglu_mlp.h:
+ *   - Element types are passed as a swiglu_dtype.  Sums, statistics and
+ *     gradients of weights are held in 32 bits or more and rounded once.
+ *   - Tensors need the alignment of their elements only.
+ *   - Calls are asynchronous on `stream`; nothing is allocated, nothing is
+ *     synchronised, no work is left behind and nothing is kept between calls.
+ *     Results do not depend on timing: the same inputs give the same bits.
+ *   - All argument checks run on the host before any HIP call, in this order:
+ *     shapes and types, null pointers, alignment, workspace size, overlap.
+ *     On any error nothing is launched.
+ */
+#ifndef SWIGLU_BLOCK_H
+#define SWIGLU_BLOCK_H
+
+#include "swiglu_mlp.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum { SWIGLU_BF16 = 0, SWIGLU_FP16 = 1, SWIGLU_FP32 = 2 } swiglu_dtype;
+
+/* Version of this header, (major << 16) | minor: 1.0. */
+int swiglu_block_abi_version(void);
+
+/* ---------------------------------------------------------------------------
+ * Layer norm over the last dimension
+ *   mean = sum x / D,  rstd = 1 / sqrt(sum (x - mean)^2 / D + eps)
+ *   xh   = (x - mean) rstd,  y = xh * weight + bias
+ * M >= 0 rows of 1 <= D <= 2^20 elements; ld* is a tensor's row stride in
+ * elements, >= D.  dtype: x, y, dy, dres, dx.  wdtype: weight, bias and their
+ * gradients; it is dtype or SWIGLU_FP32 (else SWIGLU_ERR_UNSUPPORTED).
+ * ------------------------------------------------------------------------- */
+
+/* x [M,D] -> y [M,D], and mean and rstd (float [M], each may be NULL: not
+ * written).  weight or bias [D] may be NULL (ones, zeros). eps >= 0. */
+int swiglu_layer_norm_fwd(const void* x, int64_t ldx, const void* weight, const void* bias,
+                          void* y, int64_t ldy, float* mean, float* rstd,
+                          int64_t M, int64_t D, double eps, int dtype, int wdtype, void* stream);
+
+/* Bytes of device workspace swiglu_layer_norm_bwd needs for dweight or dbias
+ * (partial sums over rows); 0 for invalid shapes. */
+size_t swiglu_layer_norm_bwd_workspace(int64_t M, int64_t D);
+
+/* With g = dy * weight:
+ *   dx = rstd (g - mean(g) - xh mean(g xh)) + dres,
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy.
+ * mean and rstd: float [M], the forward's.  weight NULL: ones.  dres [M,D]
+ * (the gradient that reaches x by another way, such as a residual branch) may
+ * be NULL; it joins in 32 bits before the one rounding.  dweight or dbias [D]
+ * may be NULL (not wanted); with M == 0 they are zeros. */
+int swiglu_layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* weight,
+                          const float* mean, const float* rstd, const void* dres, int64_t lddres,
+                          void* dx, int64_t lddx, void* dweight, void* dbias,
+                          void* ws, size_t ws_bytes,
+                          int64_t M, int64_t D, int dtype, int wdtype, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SWIGLU_BLOCK_H */

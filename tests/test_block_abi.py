@@ -1,0 +1,81 @@
+"""The entry points of include/swiglu_block.h refuse bad arguments on the host,
+before any HIP call.  CPU only: every call below is one that the library must
+refuse (or has nothing to launch for)."""
+import pytest
+import torch
+
+import bwd_gemm_epilogue_amd as sw
+
+OK, NULL, SHAPE, UNSUP, WS, ALIAS, HIP, ALIGN = 0, -1, -2, -3, -4, -5, -6, -7
+BF16, FP16, FP32 = 0, 1, 2
+
+
+def addr(i):
+    return 0x10000000 + i * (1 << 32)   # far-apart fake device addresses, never dereferenced
+
+
+def test_block_abi_version():
+    assert sw.lib().swiglu_block_abi_version() >> 16 == 1
+
+
+def test_layer_norm_fwd_refuses():
+    L = sw.lib()
+
+    def f(x=addr(0), ldx=64, w=addr(1), b=addr(2), y=addr(3), ldy=64, mean=addr(4), rstd=addr(5), M=4, D=64, eps=1e-5,
+          t=BF16, wt=FP32):
+        return L.swiglu_layer_norm_fwd(x, ldx, w, b, y, ldy, mean, rstd, M, D, eps, t, wt, None)
+    assert f(M=-1) == SHAPE
+    assert f(D=0) == SHAPE
+    assert f(D=(1 << 20) + 1, ldx=1 << 21, ldy=1 << 21) == UNSUP
+    assert f(M=1 << 31) == UNSUP
+    assert f(t=7) == UNSUP and f(wt=-1) == UNSUP
+    assert f(t=FP32, wt=BF16) == UNSUP and f(t=BF16, wt=FP16) == UNSUP
+    assert f(ldx=63) == SHAPE and f(ldy=63) == SHAPE
+    assert f(ldx=(1 << 31) + 1) == UNSUP
+    assert f(eps=-1.0) == SHAPE and f(eps=float("nan")) == SHAPE
+    assert f(x=None) == NULL and f(y=None) == NULL
+    assert f(x=addr(0) + 1) == ALIGN and f(w=addr(1) + 2) == ALIGN and f(mean=addr(4) + 2) == ALIGN
+    assert f(y=addr(0)) == ALIAS                     # in place is refused
+    assert f(y=addr(0) + 3 * 64 * 2) == ALIAS        # inside x's last row
+    assert f(mean=addr(5)) == ALIAS
+    assert f(rstd=addr(1)) == ALIAS                  # onto the weight
+    assert f(M=0, x=None, y=None, mean=None, rstd=None) == OK
+
+
+def test_layer_norm_bwd_refuses():
+    L = sw.lib()
+    M, D = 4, 64
+
+    def f(p=None, ld=(D, D, D, D), wsb=1 << 30, M=M, D=D, t=BF16, wt=FP32):
+        q = [addr(i) for i in range(10)]     # dy x weight mean rstd dres dx dweight dbias ws
+        for k, v in (p or {}).items():
+            q[k] = v
+        return L.swiglu_layer_norm_bwd(q[0], ld[0], q[1], ld[1], q[2], q[3], q[4], q[5], ld[2], q[6], ld[3], q[7], q[8],
+                                       q[9], wsb, M, D, t, wt, None)
+    assert f(M=-1) == SHAPE and f(D=0) == SHAPE
+    assert f(t=3) == UNSUP and f(t=FP16, wt=BF16) == UNSUP
+    for k in range(4):
+        ld = [D] * 4
+        ld[k] = D - 1
+        assert f(ld=ld) == SHAPE, k
+    for k in (0, 1, 3, 4, 6):
+        assert f({k: None}) == NULL, k
+    assert f({6: addr(6) + 1}) == ALIGN and f({7: addr(7) + 2}) == ALIGN and f({9: addr(9) + 4}) == ALIGN
+    need = L.swiglu_layer_norm_bwd_workspace(M, D)
+    assert need >= 4 * 2 * D * 4 or need > 0
+    assert f(wsb=need - 1) == WS and f({9: None}) == WS
+    assert f({6: addr(0)}) == ALIAS                 # dx onto dy
+    assert f({6: addr(5)}) == ALIAS                 # dx onto dres
+    assert f({8: addr(7)}) == ALIAS                 # dbias onto dweight
+    assert f({9: addr(1)}) == ALIAS                 # workspace onto x
+    assert L.swiglu_layer_norm_bwd_workspace(-1, D) == 0 and L.swiglu_layer_norm_bwd_workspace(M, 0) == 0
+
+
+def test_layer_norm_binding_refuses_host_tensors():
+    x = torch.zeros(4, 64)
+    with pytest.raises(ValueError):
+        sw.swiglu_layer_norm_fwd(x)
+    with pytest.raises(ValueError):
+        sw.swiglu_layer_norm_bwd(x, x, None, x, x)
+    with pytest.raises(ValueError):
+        sw.swiglu_layer_norm(x)

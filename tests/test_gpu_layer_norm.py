@@ -1,0 +1,311 @@
+"""Layer norm on the GPU against the definition in 64 bits.
+
+Tolerances.  e = 2^-24 is fp32's half step, u the output type's.  A sum of a
+row is a chain of at most 64 + 1 additions in a thread (D / 256 in a row wider
+than 16384), then 8 across threads; with the few operations around it every
+fp32 quantity is within K e of the sum of its terms' magnitudes, K = 100 + D /
+256.  A column's sum is a chain over at most M rows: K_w = 100 + M.  Outputs
+are rounded once, u |value|, and fp16 outputs below its normals by 2^-25."""
+import numpy as np
+import pytest
+import torch
+
+import bwd_gemm_epilogue_amd as sw
+
+pytestmark = pytest.mark.gpu
+
+E32 = 2.0 ** -24
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+EPS = 1e-5
+
+
+def half_step(t):
+    return torch.finfo(t).eps / 2
+
+
+def floor_of(t):
+    return 2.0 ** -25 if t == torch.float16 else 1e-38
+
+
+def make(M, D, t, wt, seed=0, offset=0.5, weight=True, bias=True):
+    g = torch.Generator().manual_seed(1000 * M + D + seed)
+    x = torch.randn(M, D, generator=g) * (0.5 + 2 * torch.rand(M, 1, generator=g)) + offset * torch.randn(M, 1, generator=g)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    w = (1 + 0.3 * r(D)).to(wt) if weight else None
+    b = (0.3 * r(D)).to(wt) if bias else None
+    return x.to(t), w, b, r(M, D).to(t), r(M, D).to(t)
+
+
+def check(name, got, ref, tol):
+    got, ref, tol = got.double().cpu(), ref.double(), tol.double()
+    assert got.shape == ref.shape
+    bad = ~((got - ref).abs() <= tol)
+    assert not bad.any(), (name, int(bad.sum()), float(((got - ref).abs() / tol).max()))
+
+
+def fwd_reference(x, w, b, eps=EPS):
+    x = x.double()
+    mu = x.mean(1, keepdim=True)
+    var = ((x - mu) ** 2).mean(1, keepdim=True)
+    rstd = 1 / (var + eps).sqrt()
+    xh = (x - mu) * rstd
+    w = torch.ones(x.shape[1], dtype=torch.float64) if w is None else w.double()
+    b = torch.zeros(x.shape[1], dtype=torch.float64) if b is None else b.double()
+    return mu, rstd, xh * w + b, w, b
+
+
+def check_fwd(x, w, b, y, mean, rstd, eps=EPS):
+    M, D = x.shape
+    mu, rs, ref, wd, bd = fwd_reference(x, w, b, eps)
+    K = (100 + D / 256) * E32
+    A = x.double().abs().mean(1, keepdim=True)
+    check("mean", mean, mu[:, 0], (K * A)[:, 0] + 1e-30)
+    # the mean's error enters the second moment squared
+    check("rstd", rstd, rs[:, 0], (rs * (K + (K * A * rs) ** 2))[:, 0])
+    scale = wd.abs() * rs * (x.double().abs() + mu.abs() + A)
+    check("y", y, ref, half_step(y.dtype) * ref.abs() + 2 * K * (scale + bd.abs()) + floor_of(y.dtype))
+
+
+def bwd_reference(x, w, mean, rstd, dy, res):
+    x, dy = x.double(), dy.double()
+    rs = rstd.double()[:, None]
+    xh = (x - mean.double()[:, None]) * rs
+    wd = torch.ones(x.shape[1], dtype=torch.float64) if w is None else w.double()
+    g = dy * wd
+    dx = rs * (g - g.mean(1, keepdim=True) - xh * (g * xh).mean(1, keepdim=True))
+    if res is not None:
+        dx = dx + res.double()
+    return dx, (dy * xh).sum(0), dy.sum(0), g, rs
+
+
+def check_bwd(x, w, mean, rstd, dy, res, dx, dw, db):
+    M, D = x.shape
+    rdx, rdw, rdb, g, rs = bwd_reference(x, w, mean, rstd, dy, res)
+    K, Kw = (100 + D / 256) * E32, (100 + M) * E32
+    X = rs * (x.double().abs() + mean.double().abs()[:, None])
+    big = rs * (g.abs() + g.abs().mean(1, keepdim=True) + X * (g.abs() * X).mean(1, keepdim=True))
+    if res is not None:
+        big = big + res.double().abs()
+    check("dx", dx, rdx, half_step(dx.dtype) * rdx.abs() + K * big + floor_of(dx.dtype))
+    if dw is not None:
+        check("dweight", dw, rdw, half_step(dw.dtype) * rdw.abs() + Kw * (dy.double().abs() * X).sum(0) + floor_of(dw.dtype))
+    if db is not None:
+        check("dbias", db, rdb, half_step(db.dtype) * rdb.abs() + Kw * dy.double().abs().sum(0) + floor_of(db.dtype))
+
+
+def cuda(*ts):
+    return [None if t is None else t.cuda() for t in ts]
+
+
+SHAPES = [(1, 1), (3, 7), (5, 8), (7, 9), (1, 64), (64, 511), (33, 512), (2, 513), (9, 1024), (4, 1025), (17, 2047),
+          (6, 2049), (70, 3584), (1, 4096), (5, 4097), (3, 8191), (4, 8192), (3, 8193), (2, 16384), (3, 16385), (2, 20001)]
+COMBOS = [("bf16", "fp32"), ("bf16", "bf16"), ("fp16", "fp32"), ("fp16", "fp16"), ("fp32", "fp32")]
+
+
+@pytest.mark.parametrize("t,wt", COMBOS)
+@pytest.mark.parametrize("M,D", SHAPES)
+def test_forward_and_backward(M, D, t, wt):
+    x, w, b, dy, res = make(M, D, TYPES[t], TYPES[wt])
+    X, W, B, DY, R = cuda(x, w, b, dy, res)
+    y, mean, rstd = sw.swiglu_layer_norm_fwd(X, W, B, EPS)
+    assert y.dtype == x.dtype and mean.dtype == rstd.dtype == torch.float32
+    check_fwd(x, w, b, y, mean, rstd)
+    m, r = mean.cpu(), rstd.cpu()
+    for dres in (None, R):
+        dx, dw, db = sw.swiglu_layer_norm_bwd(DY, X, W, mean, rstd, dres=dres)
+        assert dw.dtype == db.dtype == w.dtype
+        check_bwd(x, w, m, r, dy, None if dres is None else res, dx, dw, db)
+
+
+# more rows than one sweep of the row pass's workgroups, one for each way that rows are walked
+@pytest.mark.parametrize("M,D,t", [(4099, 64, "bf16"), (2100, 700, "fp32"), (2500, 2100, "fp16"), (2300, 4096, "bf16"),
+                                   (600, 3000, "fp32"), (300, 5000, "bf16"), (270, 9000, "fp32"), (280, 17000, "bf16")])
+def test_many_rows(M, D, t):
+    x, w, b, dy, res = make(M, D, TYPES[t], torch.float32)
+    X, W, B, DY, R = cuda(x, w, b, dy, res)
+    y, mean, rstd = sw.swiglu_layer_norm_fwd(X, W, B, EPS)
+    check_fwd(x, w, b, y, mean, rstd)
+    dx, dw, db = sw.swiglu_layer_norm_bwd(DY, X, W, mean, rstd, dres=R)
+    check_bwd(x, w, mean.cpu(), rstd.cpu(), dy, res, dx, dw, db)
+
+
+@pytest.mark.parametrize("weight,bias", [(False, False), (True, False), (False, True)])
+@pytest.mark.parametrize("D", [300, 6000, 17001])
+def test_without_weight_or_bias(D, weight, bias):
+    x, w, b, dy, _ = make(37, D, torch.bfloat16, torch.float32, weight=weight, bias=bias)
+    X, W, B, DY = cuda(x, w, b, dy)
+    y, mean, rstd = sw.swiglu_layer_norm_fwd(X, W, B, EPS)
+    check_fwd(x, w, b, y, mean, rstd)
+    dx, dw, db = sw.swiglu_layer_norm_bwd(DY, X, W, mean, rstd, bias_grad=bias)
+    assert (dw is None) == (not weight) and (db is None) == (not bias)
+    check_bwd(x, w, mean.cpu(), rstd.cpu(), dy, None, dx, dw, db)
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("D", [65, 1000, 4095, 5001])
+def test_row_strides_and_odd_starts(D, t):
+    """Columns of wider tensors, starting at an odd element: rows of any
+    alignment; nothing beside the outputs' rows is written."""
+    M, wide = 21, D + 13
+    x, w, b, dy, res = make(M, D, TYPES[t], torch.float32)
+
+    def inside(v, at):
+        buf = torch.full((M, wide), 7.0, dtype=v.dtype, device="cuda")
+        buf[:, at:at + D] = v.cuda()
+        return buf, buf[:, at:at + D]
+    X, DY, R = inside(x, 1)[1], inside(dy, 3)[1], inside(res, 5)[1]
+    W, B = cuda(w, b)
+    ybuf, Y = inside(torch.zeros_like(x), 7)
+    dbuf, DX = inside(torch.zeros_like(x), 11)
+    y, mean, rstd = sw.swiglu_layer_norm_fwd(X, W, B, EPS, y=Y)
+    check_fwd(x, w, b, y, mean, rstd)
+    dx, dw, db = sw.swiglu_layer_norm_bwd(DY, X, W, mean, rstd, dres=R, dx=DX)
+    check_bwd(x, w, mean.cpu(), rstd.cpu(), dy, res, dx, dw, db)
+    for buf, at in ((ybuf, 7), (dbuf, 11)):
+        assert (buf[:, :at] == 7).all() and (buf[:, at + D:] == 7).all()
+    # the same numbers as from dense tensors
+    y2, _, _ = sw.swiglu_layer_norm_fwd(x.cuda(), W, B, EPS)
+    assert torch.equal(y, y2)
+
+
+def test_offsets_past_32_bits():
+    """Rows 2^30 elements apart: the third starts 2^31 elements in."""
+    D, ld = 100, 1 << 30
+    x, w, b, dy, _ = make(3, D, torch.bfloat16, torch.float32)
+    big = torch.empty(2 * ld + D, dtype=torch.bfloat16, device="cuda")
+    X = big.as_strided((3, D), (ld, 1))
+    X.copy_(x.cuda())
+    y, mean, rstd = sw.swiglu_layer_norm_fwd(X, w.cuda(), b.cuda(), EPS)
+    check_fwd(x, w, b, y, mean, rstd)
+    dx, dw, db = sw.swiglu_layer_norm_bwd(dy.cuda(), X, w.cuda(), mean, rstd)
+    check_bwd(x, w, mean.cpu(), rstd.cpu(), dy, None, dx, dw, db)
+
+
+def test_large_offset_keeps_digits():
+    """Rows whose mean is 1000 times their spread: the second moment is taken
+    from the centred row."""
+    x, w, b, _, _ = make(9, 2000, torch.float32, torch.float32, offset=1000.0)
+    y, mean, rstd = sw.swiglu_layer_norm_fwd(*cuda(x, w, b), EPS)
+    check_fwd(x, w, b, y, mean, rstd)
+
+
+def test_constant_rows_infinities_and_nan_stay_in_their_rows():
+    x, w, b, dy, _ = make(6, 777, torch.float32, torch.float32)
+    clean = sw.swiglu_layer_norm_fwd(*cuda(x, w, b), EPS)[0].cpu()
+    x2 = x.clone()
+    x2[1] = 3.25                       # no spread: rstd = 1 / sqrt(eps), y = b
+    x2[3, 5] = float("inf")
+    x2[4, 776] = float("nan")
+    y, mean, rstd = sw.swiglu_layer_norm_fwd(*cuda(x2, w, b), EPS)
+    y = y.cpu()
+    assert torch.equal(y[[0, 2, 5]], clean[[0, 2, 5]])
+    assert torch.equal(y[1], b)
+    assert abs(float(rstd[1]) - EPS ** -0.5) <= 3 * 2.0 ** -24 * EPS ** -0.5
+    assert y[3].isnan().all() and y[4].isnan().all()
+    dx, _, _ = sw.swiglu_layer_norm_bwd(*cuda(dy, x2, w), mean, rstd)
+    assert dx.cpu()[[0, 1, 2, 5]].isfinite().all() and dx.cpu()[[3, 4]].isnan().all()
+
+
+def test_no_rows():
+    x = torch.empty(0, 96, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(96, device="cuda")
+    y, mean, rstd = sw.swiglu_layer_norm_fwd(x, w, w)
+    assert y.shape == (0, 96) and mean.shape == rstd.shape == (0,)
+    dx, dw, db = sw.swiglu_layer_norm_bwd(x, x, w, mean, rstd)
+    assert dx.shape == (0, 96) and not dw.any() and not db.any()
+
+
+def test_autograd_against_the_formula_and_differences():
+    x, w, b, dy, _ = make(12, 40, torch.float32, torch.float32)
+    leaves = [v.cuda().requires_grad_() for v in (x.reshape(3, 4, 40), w, b)]
+    sw.swiglu_layer_norm(*leaves, EPS).backward(dy.cuda().reshape(3, 4, 40))
+    ref = [v.double().requires_grad_() for v in (x, w, b)]
+    mu = ref[0].mean(1, keepdim=True)
+    y = (ref[0] - mu) / (((ref[0] - mu) ** 2).mean(1, keepdim=True) + EPS).sqrt() * ref[1] + ref[2]
+    y.backward(dy.double())
+    for got, want in zip(leaves, ref):
+        scale = want.grad.abs().max()
+        assert float((got.grad.cpu().double().reshape(want.grad.shape) - want.grad).abs().max() / scale) <= 200 * E32
+    # central differences of <y, dy> in 64 bits along random directions
+    g = torch.Generator().manual_seed(3)
+    for k, v in enumerate((x, w, b)):
+        d = torch.randn(v.shape, generator=g, dtype=torch.float64)
+
+        def f(h):
+            args = [q.double() + (h * d if i == k else 0) for i, q in enumerate((x, w, b))]
+            return float((fwd_reference(*args)[2] * dy.double()).sum())
+        want = (f(1e-5) - f(-1e-5)) / 2e-5
+        got = float((leaves[k].grad.cpu().double().reshape(v.shape) * d).sum())
+        # differences: h^2 and 2^-53 / h terms, about 1e-9 of the terms' sizes; the gradient: fp32
+        assert abs(got - want) <= 1e-5 * float((leaves[k].grad.cpu().double().reshape(v.shape) * d).abs().sum())
+
+
+def test_autograd_of_views_and_expanded_gradients():
+    base = torch.randn(6, 50, 2, device="cuda", dtype=torch.bfloat16)
+    x = base[..., 0].requires_grad_()            # last stride 2: copied
+    w = torch.ones(50, device="cuda", requires_grad=True)
+    y = sw.swiglu_layer_norm(x, w, None, EPS)
+    y.sum().backward()                           # an expanded gradient
+    _, _, db, _, _ = bwd_reference(x.detach().cpu(), None, torch.zeros(6), torch.ones(6), torch.ones(6, 50), None)
+    assert x.grad.shape == x.shape and w.grad.shape == (50,)
+    # sum over the columns of xh is zero: each entry is rounding only
+    assert float(x.grad.float().abs().max()) <= 100 * E32 * 50
+
+
+def test_same_bits_every_time_and_on_another_stream():
+    x, w, b, dy, res = make(1500, 1111, torch.bfloat16, torch.float32)
+    X, W, B, DY, R = cuda(x, w, b, dy, res)
+    y, mean, rstd = sw.swiglu_layer_norm_fwd(X, W, B)
+    first = sw.swiglu_layer_norm_bwd(DY, X, W, mean, rstd, dres=R)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        y2, m2, r2 = sw.swiglu_layer_norm_fwd(X, W, B, stream=s)
+        again = sw.swiglu_layer_norm_bwd(DY, X, W, m2, r2, dres=R, stream=s)
+        s.synchronize()
+        assert torch.equal(y, y2)
+        for p, q in zip(first, again):
+            assert torch.equal(p, q)
+
+
+def test_in_a_graph():
+    x, w, b, dy, _ = make(300, 640, torch.bfloat16, torch.float32)
+    X, W, B, DY = cuda(x, w, b, dy)
+    sw.swiglu_layer_norm_fwd(X, W, B)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        y, mean, rstd = sw.swiglu_layer_norm_fwd(X, W, B)
+        got = sw.swiglu_layer_norm_bwd(DY, X, W, mean, rstd)
+    for k in range(4):
+        X.copy_((x.float() * (k + 1) + k).to(x.dtype))
+        DY.copy_((dy.float() * (0.5 + k)).to(dy.dtype))
+        g.replay()
+        torch.cuda.synchronize()
+        ey, em, er = sw.swiglu_layer_norm_fwd(X, W, B)
+        assert torch.equal(y, ey)
+        for p, q in zip(got, sw.swiglu_layer_norm_bwd(DY, X, W, em, er)):
+            assert torch.equal(p, q)
+
+
+def test_binding_refuses_what_the_kernels_cannot_take():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(64, device="cuda")
+    stat = torch.zeros(4, device="cuda")
+    for bad in (lambda: sw.swiglu_layer_norm_fwd(x.double(), w.double()),
+                lambda: sw.swiglu_layer_norm_fwd(x, w.half()),
+                lambda: sw.swiglu_layer_norm_fwd(x, w[:63]),
+                lambda: sw.swiglu_layer_norm_fwd(x, w.cpu()),
+                lambda: sw.swiglu_layer_norm_fwd(x.t(), w[:4]),
+                lambda: sw.swiglu_layer_norm_fwd(x[0], w),
+                lambda: sw.swiglu_layer_norm_fwd(x[:1].expand(4, 64), w),
+                lambda: sw.swiglu_layer_norm_fwd(x, w, y=torch.zeros(4, 63, dtype=torch.bfloat16, device="cuda")),
+                lambda: sw.swiglu_layer_norm_bwd(x.float(), x, w, stat, stat),
+                lambda: sw.swiglu_layer_norm_bwd(x, x, w, stat[:3], stat),
+                lambda: sw.swiglu_layer_norm_bwd(x, x, w, stat, stat, ws=torch.zeros(8, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(sw.SwiGLUError):
+        sw.swiglu_layer_norm_fwd(x, w, y=x)
