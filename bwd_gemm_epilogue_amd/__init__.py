@@ -166,9 +166,17 @@ def _dev(t: torch.Tensor, name: str, shape=None) -> int:
 def _stream(t: torch.Tensor, stream) -> int:
     """The HIP stream handle of a call (inside a _launches call `stream` is
     already the torch stream the call runs on)."""
+    if type(stream) is int:
+        return stream
     if stream is None:
         stream = torch.cuda.current_stream(t.device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+# The handle of the current stream without a stream object around it (0.1 us
+# against 2.7 us of a call's host time).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _launches(fn):
@@ -191,9 +199,9 @@ def _launches(fn):
         if not isinstance(like, torch.Tensor) or not like.is_cuda:
             raise ValueError(f"{fn.__name__}: the first argument must be a tensor on a GPU (no CPU path)")
         stream = kw.get("stream")
-        if stream is None and like.device.index == torch.cuda.current_device():
-            # the device and its stream are current already
-            kw["stream"] = torch.cuda.current_stream()
+        if stream is None and like.get_device() == torch.cuda.current_device():
+            # the device and its stream are current already: the handle alone
+            kw["stream"] = _raw_stream(like.get_device())
             return fn(*args, **kw)
         if stream is None:
             st = torch.cuda.current_stream(like.device)

@@ -14,6 +14,7 @@ __all__ = [
 ]
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_F32 = torch.float32
 
 
 def _dtype(t: torch.Tensor, name: str) -> int:
@@ -23,25 +24,31 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _typed(t, name: str, shape, dtype: torch.dtype) -> int:
-    """The address of a contiguous tensor of this shape and type."""
-    _on_gpu(t, name)
+# These calls are short, so the checks are written to cost little when they
+# pass: `dev` is the index of the GPU that the call runs on, and get_device()
+# (-1 on the host) holds both questions; _on_gpu words the refusal.
+
+def _fits(t, name: str, shape, dtype, dev: int):
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _on_gpu(t, name)
+        raise ValueError(f"{name} must be on cuda:{dev}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _typed(t, name: str, shape, dtype, dev: int) -> int:
+    """The address of a contiguous tensor of this shape and type."""
+    _fits(t, name, shape, dtype, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _rows(t, name: str, shape, dtype: torch.dtype):
+def _rows(t, name: str, shape, dtype, dev: int):
     """(address, row stride in elements) of a matrix whose rows are dense."""
-    _on_gpu(t, name)
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    _fits(t, name, shape, dtype, dev)
     M, D = shape
     if D > 1 and M > 0 and t.stride(1) != 1:
         raise ValueError(f"{name} must have dense rows (last stride 1)")
@@ -55,13 +62,12 @@ def _rows(t, name: str, shape, dtype: torch.dtype):
 # layer norm
 # --------------------------------------------------------------------------
 
-def _norm_vectors(D, x, **vectors):
-    """(type of weight and bias, their addresses or None)."""
-    given = [v for v in vectors.values() if v is not None]
-    wt = given[0].dtype if given else x.dtype
-    if wt not in (x.dtype, torch.float32):
+def _norm_type(x, v):
+    """The type of weight and bias (v: one that is given, or None)."""
+    wt = x.dtype if v is None else v.dtype
+    if wt != x.dtype and wt != _F32:
         raise ValueError(f"weight and bias must be {x.dtype} or float32, got {wt}")
-    return wt, [None if v is None else _typed(v, n, (D,), wt) for n, v in vectors.items()]
+    return wt
 
 
 @_launches
@@ -71,20 +77,23 @@ def swiglu_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None
     float32 [M]."""
     if x.dim() != 2:
         raise ValueError(f"x must have two dimensions, got {tuple(x.shape)}")
-    M, D = x.shape
-    xp, ldx = _rows(x, "x", (M, D), x.dtype)
+    shape, t, dev = x.shape, x.dtype, x.get_device()
+    M, D = shape
     code = _dtype(x, "x")
-    wt, (wp, bp) = _norm_vectors(D, x, weight=weight, bias=bias)
-    y = torch.empty((M, D), dtype=x.dtype, device=x.device) if y is None else y
-    stats = None
-    if mean is None and rstd is None:
-        stats = torch.empty((2, M), dtype=torch.float32, device=x.device)
-    mean = (torch.empty(M, dtype=torch.float32, device=x.device) if stats is None else stats[0]) if mean is None else mean
-    rstd = (torch.empty(M, dtype=torch.float32, device=x.device) if stats is None else stats[1]) if rstd is None else rstd
-    yp, ldy = _rows(y, "y", (M, D), x.dtype)
+    xp, ldx = _rows(x, "x", shape, t, dev)
+    wt = _norm_type(x, bias if weight is None else weight)
+    wp = None if weight is None else _typed(weight, "weight", (D,), wt, dev)
+    bp = None if bias is None else _typed(bias, "bias", (D,), wt, dev)
+    if y is None:
+        y = x.new_empty(shape)
+    if mean is None:
+        mean = x.new_empty(M, dtype=_F32)
+    if rstd is None:
+        rstd = x.new_empty(M, dtype=_F32)
+    yp, ldy = _rows(y, "y", shape, t, dev)
     _check("swiglu_layer_norm_fwd", lib().swiglu_layer_norm_fwd(
-        xp, ldx, wp, bp, yp, ldy, _typed(mean, "mean", (M,), torch.float32),
-        _typed(rstd, "rstd", (M,), torch.float32), M, D, eps, code, _DTYPES[wt], _stream(x, stream)))
+        xp, ldx, wp, bp, yp, ldy, _typed(mean, "mean", (M,), _F32, dev), _typed(rstd, "rstd", (M,), _F32, dev),
+        M, D, eps, code, _DTYPES[wt], _stream(x, stream)))
     return y, mean, rstd
 
 
@@ -101,21 +110,30 @@ def swiglu_layer_norm_bwd(dy, x, weight, mean, rstd, dres=None, bias_grad=True, 
     weight's, or x's where there is none)."""
     if x.dim() != 2:
         raise ValueError(f"x must have two dimensions, got {tuple(x.shape)}")
-    M, D = x.shape
+    shape, t, dev = x.shape, x.dtype, x.get_device()
+    M, D = shape
     code = _dtype(x, "x")
-    dyp, lddy = _rows(dy, "dy", (M, D), x.dtype)
-    xp, ldx = _rows(x, "x", (M, D), x.dtype)
-    rp, ldr = (None, D) if dres is None else _rows(dres, "dres", (M, D), x.dtype)
-    if weight is not None and dweight is None:
-        dweight = torch.empty(D, dtype=weight.dtype, device=x.device)
+    dyp, lddy = _rows(dy, "dy", shape, t, dev)
+    xp, ldx = _rows(x, "x", shape, t, dev)
+    rp, ldr = (None, D) if dres is None else _rows(dres, "dres", shape, t, dev)
+    wt = _norm_type(x, next((v for v in (weight, dweight, dbias) if v is not None), None))
+    wp = dwp = dbp = None
+    if weight is not None:
+        wp = _typed(weight, "weight", (D,), wt, dev)
+        if dweight is None:
+            dweight = weight.new_empty(D)
     if bias_grad and dbias is None:
-        dbias = torch.empty(D, dtype=x.dtype if weight is None else weight.dtype, device=x.device)
-    wt, (wp, dwp, dbp) = _norm_vectors(D, x, weight=weight, dweight=dweight, dbias=dbias)
-    dx = torch.empty((M, D), dtype=x.dtype, device=x.device) if dx is None else dx
-    dxp, lddx = _rows(dx, "dx", (M, D), x.dtype)
+        dbias = x.new_empty(D, dtype=wt)
+    if dweight is not None:
+        dwp = _typed(dweight, "dweight", (D,), wt, dev)
+    if dbias is not None:
+        dbp = _typed(dbias, "dbias", (D,), wt, dev)
+    if dx is None:
+        dx = x.new_empty(shape)
+    dxp, lddx = _rows(dx, "dx", shape, t, dev)
     ws = _ws(swiglu_layer_norm_bwd_workspace(M, D) if dwp or dbp else 0, x, ws)
     _check("swiglu_layer_norm_bwd", lib().swiglu_layer_norm_bwd(
-        dyp, lddy, xp, ldx, wp, _typed(mean, "mean", (M,), torch.float32), _typed(rstd, "rstd", (M,), torch.float32),
+        dyp, lddy, xp, ldx, wp, _typed(mean, "mean", (M,), _F32, dev), _typed(rstd, "rstd", (M,), _F32, dev),
         rp, ldr, dxp, lddx, dwp, dbp, ws.data_ptr(), ws.numel() * ws.element_size(), M, D, code, _DTYPES[wt],
         _stream(x, stream)))
     return dx, dweight, dbias

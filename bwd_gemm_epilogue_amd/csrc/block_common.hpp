@@ -37,6 +37,12 @@ template <class T>
 __device__ __forceinline__ void store_vec(T* p, typename Vec<T>::type v) {
   *(typename Vec<T>::loose*)p = v;
 }
+// The same as a streaming (nontemporal) store: the output does not push the
+// inputs of later work out of the caches.
+template <class T>
+__device__ __forceinline__ void stream_vec(T* p, typename Vec<T>::type v) {
+  __builtin_nontemporal_store(v, (typename Vec<T>::loose*)p);
+}
 // N values of type W as floats, N a multiple of W's vector
 template <int N, class W>
 __device__ __forceinline__ void load_floats(const W* p, float (&f)[N]) {
