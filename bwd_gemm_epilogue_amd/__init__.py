@@ -87,6 +87,8 @@ _SIGNATURES = {
     "swiglu_layer_norm_bwd_workspace": (_SZ, [_I64] * 2),
     "swiglu_layer_norm_bwd": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P, _P, _P, _SZ,
                                              _I64, _I64, _INT, _INT, _P]),
+    "swiglu_clip_grad_norm_workspace": (_SZ, [_I64]),
+    "swiglu_clip_grad_norm": (ctypes.c_int, [_P] * 4 + [_I64, _F64, _P, _P, _SZ, _P]),
 }
 
 
@@ -180,8 +182,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 
 def _launches(fn):
-    """Run a launching call with its first tensor's device current and the
-    launch stream as torch's current stream.  Every tensor the call
+    """Run a launching call with its first tensor's device (or that of the
+    first tensor of its first list) current and the launch stream as torch's current stream.  Every tensor the call
     allocates (outputs, a temporary workspace) then belongs to that stream in
     the caching allocator, so a temporary freed on return is not handed to
     other work before the launched kernels are done with it.  `stream` may
@@ -196,6 +198,8 @@ def _launches(fn):
             kw["stream"] = args[at]
             args = args[:at]
         like = args[0] if args else None
+        if isinstance(like, (list, tuple)):
+            like = next((t for t in like if t is not None), None)
         if not isinstance(like, torch.Tensor) or not like.is_cuda:
             raise ValueError(f"{fn.__name__}: the first argument must be a tensor on a GPU (no CPU path)")
         stream = kw.get("stream")

@@ -4,6 +4,9 @@ function marshals arguments only; the arithmetic runs in the HIP kernels and
 there is no CPU path."""
 from __future__ import annotations
 
+import ctypes
+import math
+
 import torch
 
 from . import _check, _launches, _on_gpu, _stream, _ws, lib
@@ -11,6 +14,7 @@ from . import _check, _launches, _on_gpu, _stream, _ws, lib
 __all__ = [
     "swiglu_layer_norm_fwd", "swiglu_layer_norm_bwd", "swiglu_layer_norm_bwd_workspace",
     "SwiGLULayerNormFunction", "swiglu_layer_norm",
+    "swiglu_clip_grad_norm", "swiglu_clip_grad_norm_workspace", "swiglu_grad_norm",
 ]
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
@@ -171,3 +175,70 @@ class SwiGLULayerNormFunction(torch.autograd.Function):
 
 def swiglu_layer_norm(x, weight=None, bias=None, eps=1e-5):
     return SwiGLULayerNormFunction.apply(x, weight, bias, eps)
+
+
+# --------------------------------------------------------------------------
+# global gradient norm and clipping
+# --------------------------------------------------------------------------
+
+def swiglu_clip_grad_norm_workspace(n) -> int:
+    return lib().swiglu_clip_grad_norm_workspace(n)
+
+
+def _addresses(tensors, name: str, dev: int):
+    """The addresses of contiguous tensors on this GPU, and their types."""
+    codes = []
+    for t in tensors:
+        if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+            _on_gpu(t, name)
+            raise ValueError(f"every tensor of {name} must be on cuda:{dev}")
+        if not t.is_contiguous():
+            raise ValueError(f"every tensor of {name} must be contiguous")
+        code = _DTYPES.get(t.dtype)
+        if code is None:
+            raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+        codes.append(code)
+    return [t.data_ptr() for t in tensors], codes
+
+
+def _clip(grads, max_norm, outs, total, ws, stream):
+    if isinstance(grads, torch.Tensor):
+        grads, outs = [grads], None if outs is None else [outs]
+    if outs is not None and len(outs) != len(grads):
+        raise ValueError(f"{len(outs)} outs for {len(grads)} gradients")
+    if outs is not None:
+        outs = [o for o, g in zip(outs, grads) if g is not None]
+    grads = [g for g in grads if g is not None]
+    like, n = grads[0], len(grads)
+    dev = like.get_device()
+    ptrs, codes = _addresses(grads, "grads", dev)
+    numels = [g.numel() for g in grads]
+    out_array = None
+    if outs is not None:
+        optrs, ocodes = _addresses(outs, "outs", dev)
+        if ocodes != codes or [o.numel() for o in outs] != numels:
+            raise ValueError("every tensor of outs must have its gradient's type and size")
+        out_array = (ctypes.c_void_p * n)(*optrs)
+    if total is None:
+        total = like.new_empty((), dtype=_F32)
+    ws = _ws(swiglu_clip_grad_norm_workspace(n), like, ws)
+    _check("swiglu_clip_grad_norm", lib().swiglu_clip_grad_norm(
+        (ctypes.c_void_p * n)(*ptrs), out_array, (ctypes.c_int64 * n)(*numels), (ctypes.c_int * n)(*codes), n, max_norm,
+        _typed(total, "total", (), _F32, dev), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(like, stream)))
+    return total
+
+
+@_launches
+def swiglu_clip_grad_norm(grads, max_norm, outs=None, total=None, ws=None, stream=None):
+    """Scale the gradients (a list of contiguous tensors of any sizes and of
+    bfloat16, float16 or float32; None entries are passed over) by min(1,
+    max_norm / (total + 1e-6)), total the 2-norm of all of them together, in
+    place or into `outs`.  Returns total, a float32 scalar on the GPU: the
+    host does not wait."""
+    return _clip(grads, max_norm, outs, total, ws, stream)
+
+
+@_launches
+def swiglu_grad_norm(grads, total=None, ws=None, stream=None):
+    """The 2-norm of all gradients together, a float32 scalar on the GPU."""
+    return _clip(grads, math.inf, None, total, ws, stream)

@@ -1,7 +1,8 @@
 /*
  * swiglu_block.h -- C ABI of the operators around the SwiGLU MLP step
  * (swiglu_mlp.h) in a block that trains or serves it, on MI355X (gfx950):
- *   - layer norm, forward and backward (in front of the MLP).
+ *   - layer norm, forward and backward (in front of the MLP);
+ *   - the global gradient norm and clipping (behind the backward).
  *
  * Conventions, where they are not those of swiglu_mlp.h:
  *   - Element types are passed as a swiglu_dtype.  Sums, statistics and
@@ -59,6 +60,28 @@ int swiglu_layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t l
                           void* dx, int64_t lddx, void* dweight, void* dbias,
                           void* ws, size_t ws_bytes,
                           int64_t M, int64_t D, int dtype, int wdtype, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Global gradient norm and clipping
+ *   total = sqrt(sum over all tensors and elements of g^2)
+ *   c     = min(1, max_norm / (total + 1e-6)),  out = rn(c * g)
+ * ------------------------------------------------------------------------- */
+
+/* Bytes of device workspace swiglu_clip_grad_norm needs for n tensors
+ * (partial sums); 0 for invalid n. */
+size_t swiglu_clip_grad_norm_workspace(int64_t n);
+
+/* grads, outs, numels, dtypes: HOST arrays of 0 <= n <= 2^20 entries, read
+ * during the call: the device pointer of gradient i, that of its output, its
+ * elements (>= 0; at most 2^40 in all tensors together), its swiglu_dtype.
+ * outs[i] has grads[i]'s type; it is grads[i] (in place) or overlaps no
+ * gradient and no other output; outs NULL: all in place.  total: float
+ * [1] on the device.  The sum of squares is held in 64 bits, so no finite
+ * gradient overflows it.  In place with c == 1 nothing is written.  A total
+ * that is infinite gives c = 0, one that is NaN gives c = NaN.  max_norm >= 0;
+ * infinity: the norm alone (outs must be NULL or in place). */
+int swiglu_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes,
+                          int64_t n, double max_norm, float* total, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -79,3 +79,54 @@ def test_layer_norm_binding_refuses_host_tensors():
         sw.swiglu_layer_norm_bwd(x, x, None, x, x)
     with pytest.raises(ValueError):
         sw.swiglu_layer_norm(x)
+
+
+def _clip(grads=(addr(0), addr(1)), outs=None, numels=(64, 7), dtypes=(BF16, FP32), n=2, max_norm=1.0, total=addr(8),
+          ws=addr(9), wsb=1 << 30):
+    import ctypes
+    arr = lambda t, v: None if v is None else (t * max(1, len(v)))(*v)  # noqa: E731
+    return sw.lib().swiglu_clip_grad_norm(arr(ctypes.c_void_p, grads), arr(ctypes.c_void_p, outs),
+                                          arr(ctypes.c_int64, numels), arr(ctypes.c_int, dtypes), n, max_norm, total,
+                                          ws, wsb, None)
+
+
+def test_clip_refuses():
+    L = sw.lib()
+    assert _clip(n=-1) == SHAPE and _clip(max_norm=-1.0) == SHAPE and _clip(max_norm=float("nan")) == SHAPE
+    assert _clip(n=(1 << 20) + 1) == UNSUP
+    assert _clip(numels=(64, -7)) == SHAPE
+    assert _clip(numels=(64, (1 << 40) + 1)) == UNSUP and _clip(numels=(1 << 40, 1 << 40)) == UNSUP
+    assert _clip(dtypes=(BF16, 3)) == UNSUP
+    assert _clip(grads=None) == NULL and _clip(numels=None) == NULL and _clip(dtypes=None) == NULL
+    assert _clip(total=None) == NULL
+    assert _clip(grads=(addr(0), None)) == NULL and _clip(outs=(addr(2), None)) == NULL
+    assert _clip(grads=(addr(0) + 1, addr(1))) == ALIGN and _clip(grads=(addr(0), addr(1) + 2)) == ALIGN
+    assert _clip(outs=(addr(2), addr(3) + 1)) == ALIGN and _clip(total=addr(8) + 2) == ALIGN
+    assert _clip(ws=addr(9) + 8) == ALIGN
+    assert _clip(ws=None) == WS and _clip(wsb=L.swiglu_clip_grad_norm_workspace(2) - 1) == WS
+    assert L.swiglu_clip_grad_norm_workspace(-1) == 0
+    assert L.swiglu_clip_grad_norm_workspace(1000) > L.swiglu_clip_grad_norm_workspace(1) > 0
+    # the same gradient twice in place, and one that starts inside another
+    assert _clip(grads=(addr(0), addr(0))) == ALIAS
+    assert _clip(grads=(addr(0), addr(0) + 126), dtypes=(BF16, BF16)) == ALIAS
+    # an output on another gradient, two outputs on each other, outputs on total or the workspace
+    assert _clip(outs=(addr(1), addr(3))) == ALIAS
+    assert _clip(outs=(addr(2), addr(2) + 4)) == ALIAS
+    assert _clip(outs=(addr(2), addr(8) - 4)) == ALIAS
+    assert _clip(outs=(addr(9) + 64, addr(3))) == ALIAS
+    assert _clip(total=addr(0)) == ALIAS and _clip(total=addr(9)) == ALIAS
+    # partly inside one another: the output begins before the gradient ends
+    assert _clip(outs=(addr(0) + 64, addr(3))) == ALIAS
+    # the norm alone has nothing to write into
+    assert _clip(max_norm=float("inf"), outs=(addr(2), addr(3))) == UNSUP
+
+
+def test_clip_binding_refuses_host_tensors_and_nothing():
+    with pytest.raises(ValueError):
+        sw.swiglu_clip_grad_norm([torch.zeros(4)], 1.0)
+    with pytest.raises(ValueError):
+        sw.swiglu_clip_grad_norm([], 1.0)
+    with pytest.raises(ValueError):
+        sw.swiglu_clip_grad_norm([None], 1.0)
+    with pytest.raises(ValueError):
+        sw.swiglu_grad_norm(torch.zeros(4))

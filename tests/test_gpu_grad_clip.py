@@ -1,0 +1,234 @@
+"""The global gradient norm and clipping on the GPU against the definition in
+64 bits.
+
+Tolerances.  The sum of squares is held in 64 bits, so the total is rounded
+once: half a step of fp32, 2^-24, with as much again for the order of the
+sum's last digits.  The factor is rounded once to fp32 (2^-24), its product
+with the gradient once to fp32 and once to the gradient's type: u + 3 * 2^-24
+relative, and half of fp16's smallest step."""
+import math
+
+import pytest
+import torch
+
+import bwd_gemm_epilogue_amd as sw
+
+pytestmark = pytest.mark.gpu
+
+E32 = 2.0 ** -24
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def make(sizes, types, seed=0, std=1e-2):
+    g = torch.Generator().manual_seed(seed)
+    return [(torch.randn(n, generator=g) * std).to(types[i % len(types)]) for i, n in enumerate(sizes)]
+
+
+def norm64(grads):
+    return math.sqrt(sum(float(g.double().square().sum()) for g in grads))
+
+
+def check(grads, got, total, max_norm):
+    want = norm64(grads)
+    assert total.dtype == FP32 and total.dim() == 0
+    assert abs(float(total) - want) <= 2 * E32 * want
+    c = min(1.0, max_norm / (want + 1e-6))
+    for k, (g, o) in enumerate(zip(grads, got)):
+        assert o.dtype == g.dtype and o.shape == g.shape
+        o = o.cpu()
+        if c == 1.0:
+            assert torch.equal(o, g), k
+            continue
+        ref = g.double() * c
+        u = torch.finfo(g.dtype).eps / 2
+        tol = (u + 3 * E32) * ref.abs() + (2.0 ** -25 if g.dtype == FP16 else 0.0)
+        assert ((o.double() - ref).abs() <= tol).all(), k
+
+
+SETS = [
+    ([1], [BF16]), ([0], [FP32]), ([0, 0, 5, 0], [FP16]), ([7, 8, 9], [FP32]), ([2047, 2048, 2049], [BF16]),
+    ([1, 0, 3, 100000, 17, 0], [BF16, FP32, FP16]), ([65536, 65537, 3], [FP16, FP32]),
+    ([3_000_001], [BF16]), ([5_000_000, 1, 4_000_003], [FP32, BF16]),
+    (list(range(1, 129)), [FP32]), (list(range(0, 129)), [BF16]), ([5] * 257, [BF16, FP32, FP16]),
+    ([1000 + 37 * i for i in range(300)], [FP32, BF16]),
+]
+
+
+@pytest.mark.parametrize("factor", [0.3, 5.0])
+@pytest.mark.parametrize("k", range(len(SETS)))
+def test_norm_and_clipping(k, factor):
+    grads = make(*SETS[k], seed=k)
+    max_norm = factor * norm64(grads)
+    if norm64(grads) < 1e-3:
+        max_norm = factor          # a norm near zero: never clipped
+    d = [g.cuda() for g in grads]
+    assert abs(float(sw.swiglu_grad_norm(d)) - norm64(grads)) <= 2 * E32 * norm64(grads)
+    outs = [torch.full_like(g, 3.0) for g in d]
+    total = sw.swiglu_clip_grad_norm(d, max_norm, outs=outs)
+    check(grads, outs, total, max_norm)
+    check(grads, d, total, math.inf)              # the gradients are as they were
+    total = sw.swiglu_clip_grad_norm(d, max_norm)  # in place
+    check(grads, d, total, max_norm)
+
+
+@pytest.mark.parametrize("t", [BF16, FP16, FP32])
+def test_views_of_a_bucket_at_odd_starts(t):
+    """Tensors one after another in a flat buffer: any alignment, and nothing
+    between or beside them is written."""
+    sizes = [1, 3, 4097, 8, 70001, 5, 2]
+    grads = make(sizes, [t], seed=5)
+    gap = 3
+    flat = torch.full((sum(sizes) + gap * (len(sizes) + 1),), 9.0, dtype=t, device="cuda")
+    out = flat.clone()
+    at, ins, outs, inside = gap, [], [], torch.zeros(flat.shape, dtype=torch.bool, device="cuda")
+    for g in grads:
+        ins.append(flat[at:at + g.numel()])
+        outs.append(out[at:at + g.numel()])
+        ins[-1].copy_(g)
+        inside[at:at + g.numel()] = True
+        at += g.numel() + gap
+    max_norm = 0.1 * norm64(grads)
+    total = sw.swiglu_clip_grad_norm(ins, max_norm, outs=outs)
+    check(grads, outs, total, max_norm)
+    assert (out[~inside] == 9).all() and (flat[~inside] == 9).all()
+    total = sw.swiglu_clip_grad_norm(ins, max_norm)
+    check(grads, ins, total, max_norm)
+    assert (flat[~inside] == 9).all()
+
+
+def test_shapes_none_entries_and_mixed_places():
+    grads = make([64 * 64, 4097, 64], [FP32])
+    d = [grads[0].cuda().reshape(64, 64), None, grads[1].cuda(), grads[2].cuda().reshape(1, 64, 1)]
+    other = torch.empty_like(d[2])
+    max_norm = 0.5 * norm64(grads)
+    total = sw.swiglu_clip_grad_norm(d, max_norm, outs=[d[0], None, other, d[3]])
+    check(grads, [d[0].reshape(-1), other, d[3].reshape(-1)], total, max_norm)
+    assert torch.equal(d[2].cpu(), grads[1])
+
+
+def test_values_whose_squares_leave_32_bits():
+    for t, v in ((BF16, 2.0 ** 100), (FP32, 1e-30), (FP32, 3e38), (BF16, 1e-38)):
+        g = torch.full((1000,), v).to(t)
+        total = sw.swiglu_grad_norm([g.cuda()])
+        want = norm64([g])
+        if want > torch.finfo(FP32).max:
+            assert float(total) == math.inf        # the norm itself is past fp32
+        else:
+            assert abs(float(total) - want) <= 2 * E32 * want
+    # past fp32's range only as a float: the factor comes from the 64-bit norm.  It
+    # is below fp32's normals there, off by half their smallest step
+    g = torch.full((1000,), 3e38)
+    out = sw_clip_to(g, 1.0)
+    ref = g.double() / norm64([g])
+    assert ((out.double() - ref).abs() <= 4 * E32 * ref + g.double() * 2.0 ** -150).all()
+
+
+def sw_clip_to(g, max_norm):
+    d = g.cuda()
+    sw.swiglu_clip_grad_norm([d], max_norm)
+    return d.cpu()
+
+
+def test_infinite_and_nan_gradients():
+    g = make([5000, 300], [FP32])
+    a = [v.clone() for v in g]
+    a[0][17] = float("inf")
+    d = [v.cuda() for v in a]
+    total = sw.swiglu_clip_grad_norm(d, 1.0)
+    assert float(total) == math.inf
+    got = d[0].cpu()
+    assert got[17].isnan() and (got[:17] == 0).all() and (d[1] == 0).all()
+    a[1][3] = float("nan")
+    d = [v.cuda() for v in a]
+    assert math.isnan(float(sw.swiglu_clip_grad_norm(d, 1.0)))
+    assert all(v.isnan().all() for v in d)
+
+
+def test_zero_gradients_and_zero_max_norm():
+    z = torch.zeros(999, device="cuda")
+    assert float(sw.swiglu_clip_grad_norm([z], 1.0)) == 0.0 and not z.any()
+    g = make([999], [BF16])[0].cuda()
+    sw.swiglu_clip_grad_norm([g], 0.0)
+    assert not g.any()
+
+
+def test_one_tensor_past_32_bit_offsets():
+    """2^31 + 5 elements in bf16, all zeros but a few at the ends."""
+    n = (1 << 31) + 5
+    g = torch.zeros(n, dtype=BF16, device="cuda")
+    g[0], g[n // 2], g[n - 1], g[n - 2] = 3.0, 4.0, 12.0, 84.0
+    total = sw.swiglu_clip_grad_norm([g], 8.5)
+    assert abs(float(total) - math.sqrt(9 + 16 + 144 + 84 ** 2)) <= 2 * E32 * 86
+    c = 8.5 / (math.sqrt(9 + 16 + 144 + 84 ** 2) + 1e-6)
+    for at, v in ((0, 3.0), (n // 2, 4.0), (n - 1, 12.0), (n - 2, 84.0)):
+        assert abs(float(g[at]) - c * v) <= (2.0 ** -8 + 3 * E32) * c * v
+
+
+def test_same_bits_every_time_and_on_another_stream():
+    grads = make([100_001] * 5 + [33] * 200, [BF16, FP32], seed=9)
+    d = [g.cuda() for g in grads]
+    outs = [torch.empty_like(g) for g in d]
+    first = sw.swiglu_clip_grad_norm(d, 1e-3, outs=outs).clone()
+    keep = [o.clone() for o in outs]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        total = sw.swiglu_clip_grad_norm(d, 1e-3, outs=outs, stream=s)
+        s.synchronize()
+        assert torch.equal(total, first) and all(torch.equal(p, q) for p, q in zip(outs, keep))
+
+
+def test_in_a_graph():
+    grads = make([4001, 128, 70000], [BF16, FP32])
+    d = [g.cuda() for g in grads]
+    outs = [torch.empty_like(g) for g in d]
+    sw.swiglu_clip_grad_norm(d, 0.1, outs=outs)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        total = sw.swiglu_clip_grad_norm(d, 0.1, outs=outs)
+    for k in range(4):
+        now = [(g.float() * (0.2 + k)).to(g.dtype) for g in grads]
+        for a, b in zip(d, now):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(now, outs, total, 0.1)
+        again = [torch.empty_like(g) for g in d]
+        assert torch.equal(sw.swiglu_clip_grad_norm(d, 0.1, outs=again), total)
+        assert all(torch.equal(p, q) for p, q in zip(outs, again))
+
+
+def test_against_differences():
+    """Clipping is the projection g -> max_norm g / |g| outside the ball: a
+    small change along g is scaled away, one across it is scaled by the factor."""
+    g = make([2000], [FP32], std=1.0)[0]
+    n = norm64([g])
+    a, b = sw_clip_to(g, 1.0), sw_clip_to((g.double() * 1.01).float(), 1.0)
+    assert ((a.double() - b.double()).abs() <= 8 * E32 * a.double().abs()).all()
+    t = torch.randn(2000, generator=torch.Generator().manual_seed(1), dtype=torch.float64)
+    t -= (t @ g.double()) / (n * n) * g.double()
+    h = 1e-3
+    d = (sw_clip_to((g.double() + h * t).float(), 1.0).double() - a.double()) / h
+    # second order in h, and the roundings of g + h t, of c and of the products over h
+    tol = h * float(t.square().sum()) / n ** 2 * (g.abs().double() / n + t.abs()) + 8 * E32 * (g.abs().double() + 1e-3) / n / h
+    assert ((d - t / n).abs() <= tol).all()
+
+
+def test_refusals_on_the_gpu():
+    g = torch.zeros(64, device="cuda")
+    for bad in (lambda: sw.swiglu_clip_grad_norm([g, g.cpu()], 1.0),
+                lambda: sw.swiglu_clip_grad_norm([g.double()], 1.0),
+                lambda: sw.swiglu_clip_grad_norm([g.reshape(8, 8).t()], 1.0),
+                lambda: sw.swiglu_clip_grad_norm([g], 1.0, outs=[]),
+                lambda: sw.swiglu_clip_grad_norm([g], 1.0, outs=[g.half()]),
+                lambda: sw.swiglu_clip_grad_norm([g], 1.0, outs=[g[:32].clone()]),
+                lambda: sw.swiglu_clip_grad_norm([g], 1.0, ws=torch.zeros(16, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: sw.swiglu_clip_grad_norm([g, g], 1.0), lambda: sw.swiglu_clip_grad_norm([g], -1.0),
+                lambda: sw.swiglu_clip_grad_norm([g[:60]], 1.0, outs=[g[4:]])):
+        with pytest.raises(sw.SwiGLUError):
+            bad()
