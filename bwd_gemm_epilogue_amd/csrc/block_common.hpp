@@ -43,6 +43,11 @@ template <class T>
 __device__ __forceinline__ void stream_vec(T* p, typename Vec<T>::type v) {
   __builtin_nontemporal_store(v, (typename Vec<T>::loose*)p);
 }
+// A load of data that is not read again soon.
+template <class T>
+__device__ __forceinline__ typename Vec<T>::type last_vec(const T* p) {
+  return __builtin_nontemporal_load((const typename Vec<T>::loose*)p);
+}
 // N values of type W as floats, N a multiple of W's vector
 template <int N, class W>
 __device__ __forceinline__ void load_floats(const W* p, float (&f)[N]) {

@@ -7,9 +7,11 @@
 // Bound by HBM: the norm reads every gradient once; clipping reads it again
 // (the factor depends on all of them) and writes it.  The tensors are cut into
 // chunks of one size, and workgroups walk the chunks of all tensors, so that
-// the work is even whatever the tensors' sizes.  The table of tensors travels
-// in the kernel's arguments: nothing is copied to the device or kept for a
-// later call, and a captured graph holds its own.
+// the work is even whatever the tensors' sizes.  The table of up to 128 tensors
+// travels in the kernel's arguments; a longer one is first written to the
+// workspace, 128 tensors to a launch, by kernels that take it the same way.
+// So nothing is copied from host memory or kept for a later call, and a
+// captured graph holds its own table.
 #include <new>
 
 #include <algorithm>
@@ -18,25 +20,56 @@
 
 namespace swb {
 
-constexpr int kTensors = 128;      // of one launch: 29 bytes each within 4 KB of arguments
-constexpr int kNormGroups = 1024;  // workgroups of one launch, each with one partial sum
+constexpr int kTensors = 128;   // of one table: 29 bytes each within 4 KB of arguments
+// Workgroups of a pass at most, each with one partial sum.  1024, 2048, 4096:
+// 626, 619, 600 us to clip 1.23 GB.
+constexpr int kGroups = 4096;
 
 struct Table {
   const void* in[kTensors];
   void* out[kTensors];
   int64_t n[kTensors];
-  int first[kTensors + 1];  // tensor i has chunks first[i] .. first[i + 1] - 1
+  int first[kTensors + 1];  // tensor i has chunks first[i] .. first[i + 1] - 1, counted over all tables
   uint8_t type[kTensors];
   int count, chunk;  // tensors; elements of a chunk
 };
 
-// the tensor of chunk c: the last one whose first chunk is not past c.  Every
-// lane looks at two entries; empty tensors are never the last such one.
-__device__ __forceinline__ int tensor_of(const Table& t, int c) {
+// A longer list of tensors: tables one after another in device memory.
+__global__ void __launch_bounds__(256) table_kernel(const Table t, Table* to) {
+  for (int i = threadIdx.x; i < (int)(sizeof(Table) / 4); i += 256) ((uint32_t*)to)[i] = ((const uint32_t*)&t)[i];
+}
+
+// The piece of chunk c.
+struct Piece {
+  const void* in;
+  void* out;
+  int64_t at;
+  int n, type;
+};
+
+// The tensor of chunk c is the last one whose first chunk is not past c (an
+// empty tensor, whose successor has the same first chunk, is never it): every
+// lane looks at two entries.
+__device__ __forceinline__ Piece piece_of(const Table& t, int c) {
   const int lane = threadIdx.x & 63;
   const bool a = lane < t.count && t.first[lane] <= c;
   const bool b = lane + 64 < t.count && t.first[lane + 64] <= c;
-  return __popcll(__ballot(a)) + __popcll(__ballot(b)) - 1;
+  const int i = __builtin_amdgcn_readfirstlane(__popcll(__ballot(a)) + __popcll(__ballot(b)) - 1);
+  const int64_t at = (int64_t)(c - t.first[i]) * t.chunk, left = t.n[i] - at;
+  return {t.in[i], t.out[i], at, (int)(left < t.chunk ? left : t.chunk), (int)t.type[i]};
+}
+// the same over `tables` tables in device memory: first the last table whose
+// first chunk is not past c (tables without a chunk are followed by one that
+// starts at the same chunk, or by the end), 64 of them at a time
+__device__ __forceinline__ Piece piece_of(const Table* ts, int tables, int c) {
+  const int lane = threadIdx.x & 63;
+  int k = -1;
+  for (int k0 = 0; k0 < tables; k0 += 64) {
+    const int hits = __popcll(__ballot(k0 + lane < tables && ts[k0 + lane].first[0] <= c));
+    k += hits;
+    if (hits < 64) break;
+  }
+  return piece_of(ts[__builtin_amdgcn_readfirstlane(k)], c);
 }
 
 template <class T>
@@ -68,41 +101,51 @@ __device__ __forceinline__ double square_sum(const T* p, int n) {
   return s[0] + s[1];
 }
 
+template <int WAVES>
 __device__ __forceinline__ double group_sum(double v, double* red) {
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
-  return (red[0] + red[1]) + (red[2] + red[3]);
+  double s = red[0];
+#pragma unroll
+  for (int i = 1; i < WAVES; ++i) s += red[i];
+  return s;
 }
 
 // part[blockIdx.x] = this workgroup's share of the sum of squares, in 64 bits:
-// no finite gradient overflows it, and a long sum loses nothing.
-__global__ void __launch_bounds__(256) grad_norm_kernel(const Table t, double* __restrict__ part) {
+// no finite gradient overflows it, and a long sum loses nothing.  (64-bit
+// arithmetic is not what bounds it: 1.23 GB of bf16 take 200 us, 6.1 TB/s.)
+template <bool FAR>
+__global__ void __launch_bounds__(256) grad_norm_kernel(const Table t, const Table* ts, int tables, int chunks,
+                                                        double* __restrict__ part) {
   __shared__ double red[4];
-  const int total = t.first[t.count];
   double s = 0.0;
-  for (int c = blockIdx.x; c < total; c += gridDim.x) {
-    const int i = __builtin_amdgcn_readfirstlane(tensor_of(t, c));
-    const int64_t at = (int64_t)(c - t.first[i]) * t.chunk;
-    const int64_t left = t.n[i] - at;
-    const int n = (int)(left < t.chunk ? left : t.chunk);
-    const int type = t.type[i];
-    if (type == SWIGLU_FP32) s += square_sum((const float*)t.in[i] + at, n);
-    else if (type == SWIGLU_BF16) s += square_sum((const bf16_t*)t.in[i] + at, n);
-    else s += square_sum((const fp16_t*)t.in[i] + at, n);
+  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+    Piece p;
+    if constexpr (FAR) p = piece_of(ts, tables, c);
+    else p = piece_of(t, c);
+    if (p.type == SWIGLU_FP32) s += square_sum((const float*)p.in + p.at, p.n);
+    else if (p.type == SWIGLU_BF16) s += square_sum((const bf16_t*)p.in + p.at, p.n);
+    else s += square_sum((const fp16_t*)p.in + p.at, p.n);
   }
-  s = group_sum(s, red);
+  s = group_sum<4>(s, red);
   if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
 // total and the factor from the parts, added in a fixed order
-__global__ void __launch_bounds__(256) grad_total_kernel(const double* __restrict__ part, int parts, double max_norm,
-                                                         float* total, float* factor) {
-  __shared__ double red[4];
-  double s = 0.0;
-  for (int p = threadIdx.x; p < parts; p += 256) s += part[p];
-  s = group_sum(s, red);
+__global__ void __launch_bounds__(1024) grad_total_kernel(const double* __restrict__ part, int parts, double max_norm,
+                                                          float* total, float* factor) {
+  __shared__ double red[16];
+  double v[kGroups / 1024], s = 0.0;
+#pragma unroll
+  for (int u = 0; u < kGroups / 1024; ++u) {
+    const int p = u * 1024 + (int)threadIdx.x;
+    v[u] = p < parts ? part[p] : 0.0;
+  }
+#pragma unroll
+  for (int u = 0; u < kGroups / 1024; ++u) s += v[u];
+  s = group_sum<16>(s, red);
   if (threadIdx.x == 0) {
     const double norm = __builtin_sqrt(s), q = max_norm / (norm + 1e-6);
     *total = (float)norm;
@@ -118,7 +161,7 @@ __device__ __forceinline__ void scale(const T* p, T* o, int n, float f) {
     typename Vec<T>::type r[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (v0 + 256 * u < nvec) r[u] = load_vec(p + (int64_t)(v0 + 256 * u) * VEC);
+      if (v0 + 256 * u < nvec) r[u] = last_vec(p + (int64_t)(v0 + 256 * u) * VEC);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (v0 + 256 * u < nvec) {
@@ -132,21 +175,25 @@ __device__ __forceinline__ void scale(const T* p, T* o, int n, float f) {
   if (tail < n) o[tail] = (T)((float)p[tail] * f);
 }
 
-// The chunks from the last to the first: the end of the gradients, which the
-// norm read last, is still in the last-level cache.
-__global__ void __launch_bounds__(256) grad_scale_kernel(const Table t, const float* __restrict__ factor) {
+// A workgroup's chunks are those that it had in the norm, from the last to the
+// first: what the norm read last is still in its XCD's L2 and in the last-level
+// cache (17 MB: 16.3 us against 18.3 in another order; 308 MB: 157 against 171
+// from the first chunk on).  These loads are the gradients' last use and
+// stream past the caches (in place, 308 MB: 187 -> 151 us with chunks of 16384
+// elements; 1.23 GB: 655 -> 626).
+template <bool FAR>
+__global__ void __launch_bounds__(256) grad_scale_kernel(const Table t, const Table* ts, int tables, int chunks,
+                                                         const float* __restrict__ factor) {
   const float f = *factor;
-  const int total = t.first[t.count];
-  for (int c = total - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
-    const int i = __builtin_amdgcn_readfirstlane(tensor_of(t, c));
-    if (f == 1.0f && t.in[i] == t.out[i]) continue;  // in place and unchanged
-    const int64_t at = (int64_t)(c - t.first[i]) * t.chunk;
-    const int64_t left = t.n[i] - at;
-    const int n = (int)(left < t.chunk ? left : t.chunk);
-    const int type = t.type[i];
-    if (type == SWIGLU_FP32) scale((const float*)t.in[i] + at, (float*)t.out[i] + at, n, f);
-    else if (type == SWIGLU_BF16) scale((const bf16_t*)t.in[i] + at, (bf16_t*)t.out[i] + at, n, f);
-    else scale((const fp16_t*)t.in[i] + at, (fp16_t*)t.out[i] + at, n, f);
+  for (int c = (chunks - 1) / (int)gridDim.x * (int)gridDim.x + (int)blockIdx.x; c >= 0; c -= gridDim.x) {
+    if (c >= chunks) continue;
+    Piece p;
+    if constexpr (FAR) p = piece_of(ts, tables, c);
+    else p = piece_of(t, c);
+    if (f == 1.0f && p.in == p.out) continue;  // in place and unchanged
+    if (p.type == SWIGLU_FP32) scale((const float*)p.in + p.at, (float*)p.out + p.at, p.n, f);
+    else if (p.type == SWIGLU_BF16) scale((const bf16_t*)p.in + p.at, (bf16_t*)p.out + p.at, p.n, f);
+    else scale((const fp16_t*)p.in + p.at, (fp16_t*)p.out + p.at, p.n, f);
   }
 }
 
@@ -159,10 +206,10 @@ namespace {
 
 using namespace swb;
 
-constexpr int64_t kMaxElements = (int64_t)1 << 40;  // of one tensor
+constexpr int64_t kMaxElements = (int64_t)1 << 40;  // of all tensors
 constexpr int64_t kMaxTensors = (int64_t)1 << 20;
 
-int64_t launches(int64_t n) { return (n + kTensors - 1) / kTensors; }
+int64_t table_count(int64_t n) { return (n + kTensors - 1) / kTensors; }
 
 struct Span {
   uintptr_t lo, hi;
@@ -184,11 +231,13 @@ int check_spans(Span* s, int64_t n) {
   return SWIGLU_OK;
 }
 
-// Elements of a chunk: small enough that a few tensors still fill the chip,
-// large enough that a workgroup's loop is long.
+// Elements of a chunk: one 16-byte vector of 16-bit values to a thread where
+// that already gives every workgroup one, up to eight of them (65536 elements:
+// 660 us against 650 for 1.23 GB, 8192: 637 against 626).  Past 2^42 elements
+// chunk numbers would leave 31 bits: kMaxElements.
 int chunk_of(int64_t total) {
   int64_t c = 2048;
-  while (c < 65536 && total / c > 2048) c *= 2;
+  while (c < 16384 && total / c > 2048) c *= 2;
   return (int)c;
 }
 
@@ -196,10 +245,11 @@ int chunk_of(int64_t total) {
 
 extern "C" {
 
-// a partial sum for every workgroup of every launch, then the factor
+// the workgroups' partial sums, the factor, and the tables where there are
+// several
 size_t swiglu_clip_grad_norm_workspace(int64_t n) {
   if (n < 0 || n > kMaxTensors) return 0;
-  return (size_t)launches(n) * kNormGroups * sizeof(double) + 256;
+  return kGroups * sizeof(double) + 256 + (n > kTensors ? align256((size_t)table_count(n) * sizeof(Table)) : 0);
 }
 
 int swiglu_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes,
@@ -245,43 +295,43 @@ int swiglu_clip_grad_norm(const void* const* grads, void* const* outs, const int
 
   hipStream_t st = as_stream(stream);
   double* part = (double*)ws;
-  float* factor = (float*)((char*)ws + need - 256);
+  float* factor = (float*)(part + kGroups);
+  Table* tabs = (Table*)((char*)factor + 256);
   Table t;
   t.chunk = chunk_of(elements);
-  const int64_t L = launches(n);
-  auto fill = [&](int64_t l) {
-    const int64_t i0 = l * kTensors;
+  const int tables = (int)table_count(n);
+  int64_t c = 0;  // at most 2^40 / 16384 + 2^20 chunks
+  for (int l = 0; l < tables; ++l) {
+    const int64_t i0 = (int64_t)l * kTensors;
     t.count = (int)(n - i0 < kTensors ? n - i0 : kTensors);
-    int64_t c = 0;
     for (int k = 0; k < t.count; ++k) {
       t.in[k] = grads[i0 + k];
       t.out[k] = outs ? outs[i0 + k] : (void*)grads[i0 + k];
       t.n[k] = numels[i0 + k];
       t.type[k] = (uint8_t)dtypes[i0 + k];
       t.first[k] = (int)c;
-      c += (numels[i0 + k] + t.chunk - 1) / t.chunk;  // at most 2^40 / 65536 + 128 in all
+      c += (numels[i0 + k] + t.chunk - 1) / t.chunk;
     }
     t.first[t.count] = (int)c;
-    return (int)(c < kNormGroups ? c : kNormGroups);
-  };
-  int parts = 0;
-  for (int64_t l = 0; l < L; ++l) {
-    const int groups = fill(l);
-    if (groups == 0) continue;
-    hipLaunchKernelGGL(grad_norm_kernel, dim3((unsigned)groups), dim3(256), 0, st, t, part + parts);
-    SW_TRY(launch_status());
-    parts += groups;
+    if (tables > 1) {
+      hipLaunchKernelGGL(table_kernel, dim3(1), dim3(256), 0, st, t, tabs + l);
+      SW_TRY(launch_status());
+    }
   }
-  hipLaunchKernelGGL(grad_total_kernel, dim3(1), dim3(256), 0, st, (const double*)part, parts, max_norm, total, factor);
+  const int chunks = (int)c, groups = chunks < kGroups ? chunks : kGroups;
+  if (groups > 0) {
+    auto k = tables > 1 ? grad_norm_kernel<true> : grad_norm_kernel<false>;
+    hipLaunchKernelGGL(k, dim3((unsigned)groups), dim3(256), 0, st, t, (const Table*)tabs, tables, chunks, part);
+    SW_TRY(launch_status());
+  }
+  hipLaunchKernelGGL(grad_total_kernel, dim3(1), dim3(1024), 0, st, (const double*)part, groups, max_norm, total,
+                     factor);
   SW_TRY(launch_status());
-  if (norm_only) return SWIGLU_OK;
-  for (int64_t l = L - 1; l >= 0; --l) {
-    const int groups = fill(l);
-    if (groups == 0) continue;
-    hipLaunchKernelGGL(grad_scale_kernel, dim3((unsigned)groups), dim3(256), 0, st, t, (const float*)factor);
-    SW_TRY(launch_status());
-  }
-  return SWIGLU_OK;
+  if (norm_only || groups == 0) return SWIGLU_OK;
+  auto k = tables > 1 ? grad_scale_kernel<true> : grad_scale_kernel<false>;
+  hipLaunchKernelGGL(k, dim3((unsigned)groups), dim3(256), 0, st, t, (const Table*)tabs, tables, chunks,
+                     (const float*)factor);
+  return launch_status();
 }
 
 }  // extern "C"

@@ -51,6 +51,7 @@ SETS = [
     ([3_000_001], [BF16]), ([5_000_000, 1, 4_000_003], [FP32, BF16]),
     (list(range(1, 129)), [FP32]), (list(range(0, 129)), [BF16]), ([5] * 257, [BF16, FP32, FP16]),
     ([1000 + 37 * i for i in range(300)], [FP32, BF16]),
+    ([i % 4 for i in range(9001)], [BF16, FP32]), ([0] * 8500 + [2] + [0] * 700, [FP32]),
 ]
 
 
