@@ -89,6 +89,12 @@ _SIGNATURES = {
                                              _I64, _I64, _INT, _INT, _P]),
     "swiglu_clip_grad_norm_workspace": (_SZ, [_I64]),
     "swiglu_clip_grad_norm": (ctypes.c_int, [_P] * 4 + [_I64, _F64, _P, _P, _SZ, _P]),
+    "swiglu_moe_route_workspace": (_SZ, [_I64] * 4),
+    "swiglu_moe_route": (ctypes.c_int, [_P] * 5 + [_SZ] + [_I64] * 4 + [_INT, _P]),
+    "swiglu_moe_few_workspace": (_SZ, [_I64] * 6),
+    "swiglu_moe_few_fwd": (ctypes.c_int, [_P] * 7 + [_SZ] + [_I64] * 6 + [_P]),
+    "swiglu_moe_few_layer_workspace": (_SZ, [_I64] * 6),
+    "swiglu_moe_few_layer": (ctypes.c_int, [_P] * 8 + [_SZ] + [_I64] * 6 + [_INT, _P]),
 }
 
 

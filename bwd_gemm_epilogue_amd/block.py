@@ -15,6 +15,8 @@ __all__ = [
     "swiglu_layer_norm_fwd", "swiglu_layer_norm_bwd", "swiglu_layer_norm_bwd_workspace",
     "SwiGLULayerNormFunction", "swiglu_layer_norm",
     "swiglu_clip_grad_norm", "swiglu_clip_grad_norm_workspace", "swiglu_grad_norm",
+    "swiglu_moe_route_workspace", "swiglu_moe_route", "swiglu_moe_few_workspace", "swiglu_moe_few_fwd",
+    "swiglu_moe_few_layer_workspace", "swiglu_moe_few_layer",
 ]
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
@@ -242,3 +244,93 @@ def swiglu_clip_grad_norm(grads, max_norm, outs=None, total=None, ws=None, strea
 def swiglu_grad_norm(grads, total=None, ws=None, stream=None):
     """The 2-norm of all gradients together, a float32 scalar on the GPU."""
     return _clip(grads, math.inf, None, total, ws, stream)
+
+
+# --------------------------------------------------------------------------
+# a mixture-of-experts layer for a few tokens
+# --------------------------------------------------------------------------
+
+def swiglu_moe_route_workspace(M, D, E, k) -> int:
+    return lib().swiglu_moe_route_workspace(M, D, E, k)
+
+
+def swiglu_moe_few_workspace(M, D, I, Dout, E, k) -> int:
+    return lib().swiglu_moe_few_workspace(M, D, I, Dout, E, k)
+
+
+def swiglu_moe_few_layer_workspace(M, D, I, Dout, E, k) -> int:
+    return lib().swiglu_moe_few_layer_workspace(M, D, I, Dout, E, k)
+
+
+_BF16 = torch.bfloat16
+
+
+def _matrix(x):
+    if x.dim() != 2:
+        raise ValueError(f"x must have two dimensions, got {tuple(x.shape)}")
+    return x.shape
+
+
+@_launches
+def swiglu_moe_route(x, W_router, k, renormalize=True, ids=None, weights=None, ws=None, stream=None):
+    """The k experts of each token of x [M,D] by the router W_router [D,E]:
+    (ids int32 [M,k], weights float32 [M,k])."""
+    (M, D), dev = _matrix(x), x.get_device()
+    xp = _typed(x, "x", (M, D), _BF16, dev)
+    E = W_router.shape[-1]
+    wp = _typed(W_router, "W_router", (D, E), _BF16, dev)
+    ids = x.new_empty((M, k), dtype=torch.int32) if ids is None else ids
+    weights = x.new_empty((M, k), dtype=_F32) if weights is None else weights
+    ws = _ws(swiglu_moe_route_workspace(M, D, E, k), x, ws)
+    _check("swiglu_moe_route", lib().swiglu_moe_route(
+        xp, wp, _typed(ids, "ids", (M, k), torch.int32, dev), _typed(weights, "weights", (M, k), _F32, dev),
+        ws.data_ptr(), ws.numel() * ws.element_size(), M, D, E, k, bool(renormalize), _stream(x, stream)))
+    return ids, weights
+
+
+def _experts(x, W1, W_down, dev):
+    """(M, D, I, Dout, E, address of W1, address of W_down)"""
+    M, D = _matrix(x)
+    if W1.dim() != 3 or W_down.dim() != 3:
+        raise ValueError("W1 must be [E,D,2I] and W_down [E,I,Dout]")
+    E, I, Dout = W_down.shape
+    return (M, D, I, Dout, E, _typed(W1, "W1", (E, D, 2 * I), _BF16, dev),
+            _typed(W_down, "W_down", (E, I, Dout), _BF16, dev))
+
+
+@_launches
+def swiglu_moe_few_fwd(x, W1, W_down, ids, weights, y=None, ws=None, stream=None):
+    """y[m] = sum_j weights[m,j] MLP_{ids[m,j]}(x[m]) for up to 64 tokens: x
+    [M,D], W1 [E,D,2I], W_down [E,I,Dout], ids int32 [M,k], weights float32
+    [M,k].  An id outside [0, E) adds nothing."""
+    dev = x.get_device()
+    xp = _typed(x, "x", x.shape, _BF16, dev)
+    M, D, I, Dout, E, w1p, wdp = _experts(x, W1, W_down, dev)
+    k = ids.shape[-1]
+    y = x.new_empty((M, Dout)) if y is None else y
+    ws = _ws(swiglu_moe_few_workspace(M, D, I, Dout, E, k), x, ws)
+    _check("swiglu_moe_few_fwd", lib().swiglu_moe_few_fwd(
+        xp, w1p, wdp, _typed(ids, "ids", (M, k), torch.int32, dev), _typed(weights, "weights", (M, k), _F32, dev),
+        _typed(y, "y", (M, Dout), _BF16, dev), ws.data_ptr(), ws.numel() * ws.element_size(), M, D, I, Dout, E, k,
+        _stream(x, stream)))
+    return y
+
+
+@_launches
+def swiglu_moe_few_layer(x, W_router, W1, W_down, k, renormalize=True, y=None, ids=None, weights=None, ws=None,
+                         stream=None):
+    """The whole layer for up to 64 tokens, router and experts: (y [M,Dout],
+    ids int32 [M,k], weights float32 [M,k])."""
+    dev = x.get_device()
+    xp = _typed(x, "x", x.shape, _BF16, dev)
+    M, D, I, Dout, E, w1p, wdp = _experts(x, W1, W_down, dev)
+    wrp = _typed(W_router, "W_router", (D, E), _BF16, dev)
+    y = x.new_empty((M, Dout)) if y is None else y
+    ids = x.new_empty((M, k), dtype=torch.int32) if ids is None else ids
+    weights = x.new_empty((M, k), dtype=_F32) if weights is None else weights
+    ws = _ws(swiglu_moe_few_layer_workspace(M, D, I, Dout, E, k), x, ws)
+    _check("swiglu_moe_few_layer", lib().swiglu_moe_few_layer(
+        xp, wrp, w1p, wdp, _typed(y, "y", (M, Dout), _BF16, dev), _typed(ids, "ids", (M, k), torch.int32, dev),
+        _typed(weights, "weights", (M, k), _F32, dev), ws.data_ptr(), ws.numel() * ws.element_size(),
+        M, D, I, Dout, E, k, bool(renormalize), _stream(x, stream)))
+    return y, ids, weights

@@ -33,7 +33,7 @@ FLAGS = [
 ]
 
 
-SOURCES = ["swiglu_mlp.hip", "layer_norm.hip", "grad_clip.hip"]
+SOURCES = ["swiglu_mlp.hip", "layer_norm.hip", "grad_clip.hip", "moe_few.hip"]
 
 
 def _hipcc(args, verbose: bool) -> None:

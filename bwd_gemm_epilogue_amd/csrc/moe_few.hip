@@ -1,0 +1,635 @@
+// moe_few.hip -- a whole mixture-of-experts layer for a few tokens on gfx950:
+// the router with its top-k choice, the chosen experts' SwiGLU MLPs, and the
+// weighted sum.
+//
+//   l = x Wr,  p = softmax(l),  ids = the k largest of l,  w = p[ids] (/ sum)
+//   y[m] = sum_j w[m,j] (left silu(gate)) W_down[e],  [left | gate] = x[m] W1[e],
+//   e = ids[m,j]
+//
+// With at most 64 tokens every weight is used for a few multiply-adds only, so
+// the layer is a stream of the chosen experts' weights from HBM.  A pair (token
+// m, choice j) is a row m*k + j.  Four kinds of launch:
+//   * logits: partial sums of x Wr over slices of D, in 64 bits, so that the
+//     choice does not depend on the order of the sum;
+//   * top-k: one wave to a token;
+//   * gate/up and down: a workgroup finds its expert among the ids, gathers the
+//     expert's rows, and streams one block of 128 columns of its matrix;
+//   * combine: the weighted sum of the rows' results, in a fixed order.
+#include "block_common.hpp"
+#include "swiglu_math.hpp"
+
+namespace swb {
+
+using swg::u32x4;
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kMaxPairs = 1024, kMaxExperts = 1024;
+
+// ---------------------------------------------------------------------------
+// Router
+// ---------------------------------------------------------------------------
+constexpr int kRouteTokens = 16;  // tokens of one workgroup
+constexpr int kRouteSlice = 128;  // rows of Wr of one workgroup
+
+// part[slice][m][e] = sum over the slice's d of x[m,d] Wr[d,e] in 64 bits: a
+// product of two bf16 values is exact there, and the sum is off by 2^-53 a term.
+// Thread t takes expert blockIdx.z * 256 + t % ew and every (256 / ew)-th row.
+__global__ void __launch_bounds__(256) route_logits_kernel(const uint16_t* __restrict__ x,
+                                                           const uint16_t* __restrict__ wr, double* __restrict__ part,
+                                                           int M, int D, int E) {
+  __shared__ double xs[kRouteSlice][kRouteTokens];
+  __shared__ double sums[256];
+  const int tid = threadIdx.x;
+  const int d0 = blockIdx.x * kRouteSlice, nd = min(kRouteSlice, D - d0);
+  const int m0 = blockIdx.y * kRouteTokens, nm = min(kRouteTokens, M - m0);
+  const int e0 = blockIdx.z * 256, ew = min(256, E - e0), rows = 256 / ew;
+  for (int i = tid; i < kRouteSlice * kRouteTokens; i += 256) {
+    const int m = i / kRouteSlice, d = i % kRouteSlice;
+    double v = 0.0;
+    if (m < nm && d < nd) v = (double)swg::bf16_lo(x[(int64_t)(m0 + m) * D + d0 + d]);
+    xs[d][m] = v;
+  }
+  __syncthreads();
+  const int r = tid / ew, e = tid - r * ew;
+  double acc[kRouteTokens];
+#pragma unroll
+  for (int m = 0; m < kRouteTokens; ++m) acc[m] = 0.0;
+  if (r < rows) {
+    for (int d = r; d < nd; d += rows) {
+      const double w = (double)swg::bf16_lo(wr[(int64_t)(d0 + d) * E + e0 + e]);
+#pragma unroll
+      for (int m = 0; m < kRouteTokens; ++m) acc[m] = __builtin_fma(xs[d][m], w, acc[m]);
+    }
+  }
+  for (int m = 0; m < nm; ++m) {
+    double a = 0.0;
+#pragma unroll
+    for (int q = 0; q < kRouteTokens; ++q) a = q == m ? acc[q] : a;
+    if (r < rows) sums[tid] = a;
+    __syncthreads();
+    if (r == 0) {
+      for (int q = 1; q < rows; ++q) a += sums[q * ew + e];
+      part[((int64_t)blockIdx.x * M + m0 + m) * E + e0 + e] = a;
+    }
+    __syncthreads();
+  }
+}
+
+__device__ __forceinline__ double shfl_xor_f64(double v, int d) {
+  int2 b = __builtin_bit_cast(int2, v);
+  b.x = __shfl_xor(b.x, d, 64);
+  b.y = __shfl_xor(b.y, d, 64);
+  return __builtin_bit_cast(double, b);
+}
+
+// One wave to a token.  Lane i holds experts i, i + 64, ...: the logits (the
+// slices' sums in order), their softmax, and k rounds of picking the largest
+// remaining logit.  Equal logits: the lower index.  A NaN orders as the lowest
+// and makes the token's weights NaN; the ids are valid whatever the logits.
+__global__ void __launch_bounds__(64) route_topk_kernel(const double* __restrict__ part, int slices, int M, int E,
+                                                        int k, int renorm, int* __restrict__ ids,
+                                                        float* __restrict__ weights) {
+  constexpr int PER = kMaxExperts / 64;
+  const int m = blockIdx.x, lane = threadIdx.x;
+  const double inf = __builtin_inf();
+  double l[PER];
+  double top = -inf;
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = i * 64 + lane;
+    l[i] = -inf;
+    if (e < E) {
+      double s = 0.0;
+      for (int q = 0; q < slices; ++q) s += part[((int64_t)q * M + m) * E + e];
+      nan = nan || s != s;
+      l[i] = s != s ? -inf : s;
+      top = l[i] > top ? l[i] : top;
+    }
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) {
+    const double o = shfl_xor_f64(top, d);
+    top = o > top ? o : top;
+  }
+  nan = __ballot(nan) != 0ull;
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (i * 64 + lane < E) sum += exp(l[i] - top);
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) sum += shfl_xor_f64(sum, d);
+  uint32_t taken = 0;
+  double kept = 0.0, mine = 0.0;
+  for (int j = 0; j < k; ++j) {
+    double best = -inf;
+    int at = 1 << 30;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = i * 64 + lane;
+      if (e < E && !((taken >> i) & 1u) && (at == 1 << 30 || l[i] > best)) {
+        best = l[i];
+        at = e;
+      }
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+      const double ob = shfl_xor_f64(best, d);
+      const int oa = __shfl_xor(at, d, 64);
+      if (ob > best || (ob == best && oa < at)) {
+        best = ob;
+        at = oa;
+      }
+    }
+    if ((at & 63) == lane) taken |= 1u << (at >> 6);
+    const double p = exp(best - top) / sum;
+    kept += p;
+    if (lane == j) {
+      mine = p;
+      ids[(int64_t)m * k + j] = at;
+    }
+  }
+  if (lane < k) {
+    double w = renorm ? mine / kept : mine;
+    if (nan) w = __builtin_nan("");
+    weights[(int64_t)m * k + lane] = (float)w;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The experts' matrices
+// ---------------------------------------------------------------------------
+struct FewArgs {
+  const uint16_t* x;    // gate/up: [M, K] bf16.  down: h, its upper half of bits [P, K] and then its lower half
+  const uint16_t* w;    // [E, K, N] bf16
+  const int* ids;       // [P]
+  float* part;          // [splits][P][N] partial sums
+  uint16_t* h;          // gate/up without split: [2][P][N / 2]
+  int P, E, k, K, N;
+  int splits;           // parts of K, blockIdx.z
+};
+
+struct Rows {
+  uint32_t seen[kMaxExperts / 32];
+  uint16_t row[kMaxPairs];
+};
+
+// The slot-th expert, in order of its number, that any id names, and its rows
+// in order.  False when there is no such expert (for the whole workgroup).  Ids
+// outside [0, E) name none.  Two barriers and a third after the rows.
+template <int THREADS>
+__device__ __forceinline__ bool find_expert(const FewArgs& a, int slot, Rows& sh, int& expert, int& n) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  if (tid < kMaxExperts / 32) sh.seen[tid] = 0;
+  __syncthreads();
+  for (int p = tid; p < a.P; p += THREADS) {
+    const int id = a.ids[p];
+    if ((unsigned)id < (unsigned)a.E) atomicOr(&sh.seen[id >> 5], 1u << (id & 31));
+  }
+  __syncthreads();
+  uint32_t word = lane < kMaxExperts / 32 ? sh.seen[lane] : 0u;
+  const int cnt = __popc(word);
+  int incl = cnt;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int t = __shfl_up(incl, d, 64);
+    if (lane >= d) incl += t;
+  }
+  const bool here = lane < kMaxExperts / 32 && slot >= incl - cnt && slot < incl;
+  const unsigned long long hit = __ballot(here);
+  if (hit == 0ull) return false;
+  for (int r = slot - (incl - cnt); here && r > 0; --r) word &= word - 1u;
+  const int src = __ffsll((long long)hit) - 1;
+  expert = __builtin_amdgcn_readfirstlane(__shfl(lane * 32 + __ffs((int)word) - 1, src, 64));
+  n = 0;
+  for (int p0 = 0; p0 < a.P; p0 += 64) {
+    const bool mine = p0 + lane < a.P && a.ids[p0 + lane] == expert;
+    const unsigned long long b = __ballot(mine);
+    if (tid < 64 && mine) sh.row[n + __popcll(b & ((1ull << lane) - 1ull))] = (uint16_t)(p0 + lane);
+    n += __popcll(b);
+  }
+  n = __builtin_amdgcn_readfirstlane(n);
+  __syncthreads();
+  return true;
+}
+
+__device__ __forceinline__ u32x4 stream16(const uint16_t* p) { return __builtin_nontemporal_load((const u32x4*)p); }
+
+// One workgroup: up to 16 * NT rows of one expert times 128 columns of its
+// matrix over one part of K.
+//
+// The weights go from memory to the matrix cores through registers only.  A wave
+// step covers 32 rows of W: lane l loads 16 bytes (8 columns, chunk l % 16) of
+// each of the rows 8 (l / 16) + 0..7, and so holds, for each of its 8 columns,
+// the eight consecutive k that v_mfma_f32_16x16x32_bf16 wants of column l % 16
+// in one lane; a byte permute for each pair of rows puts them together (32 for
+// the 8 KB of a step).  Product c of the 8 then covers columns 8 j + c, j = 0..15.
+// No LDS, no barrier, and two steps of loads in flight in each wave; the waves
+// take every WAVES-th step and their sums meet in LDS at the end.
+//
+// GATE: W1, columns 64 b .. + 63 of the left half beside those of the gate half
+// (chunks 8..15).  Without a split of K the workgroup has all of left and gate of
+// its channels and writes h itself, in two bf16 halves whose sum carries 16 bits
+// (the second product of the down matrix costs no time: HBM bounds it).
+template <int NT, int WAVES, bool GATE>
+__global__ void __launch_bounds__(WAVES * 64) few_kernel(const FewArgs a) {
+  __shared__ Rows sh;
+  __shared__ f32x4 sums[WAVES][8][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int expert, n;
+  if (!find_expert<WAVES * 64>(a, blockIdx.y, sh, expert, n)) return;
+  const int j = lane & 15, g = lane >> 4;
+  const int I = a.N / 2;
+  int col;  // of this lane's chunk
+  if constexpr (GATE) col = blockIdx.x * 64 + (j & 7) * 8 + (j >> 3) * I;
+  else col = min(blockIdx.x * 128 + j * 8, a.N - 8);
+  const int steps = a.K / 32;
+  const int s0 = steps * (int)blockIdx.z / a.splits, s1 = steps * ((int)blockIdx.z + 1) / a.splits;
+  const int first = s0 + wave, cnt = first < s1 ? (s1 - first + WAVES - 1) / WAVES : 0;
+  const uint16_t* wbase = a.w + (int64_t)expert * a.K * a.N + (int64_t)(g * 8) * a.N + col;
+  constexpr int PARTS = GATE ? 1 : 2;  // bf16 parts of an operand row
+
+  for (int r0 = 0; r0 < n; r0 += 16 * NT) {
+    const int nt = min(NT, (n - r0 + 15) / 16);
+    const uint16_t* xrow[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int p = sh.row[min(r0 + t * 16 + j, n - 1)];
+      xrow[t] = a.x + (int64_t)(GATE ? p / a.k : p) * a.K + g * 8;
+    }
+    f32x4 acc[NT][8];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[t][c] = f32x4{};
+    struct Step {
+      u32x4 w[8];
+      u32x4 x[NT][PARTS];
+    };
+    auto load = [&](int i, Step& q) {
+      const int64_t kk = (int64_t)(first + i * WAVES) * 32;
+      const uint16_t* p = wbase + kk * a.N;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) q.w[r] = stream16(p + (int64_t)r * a.N);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < PARTS; ++u) q.x[t][u] = *(const u32x4*)(xrow[t] + (int64_t)u * a.P * a.K + kk);
+    };
+    auto use = [&](const Step& q) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        u32x4 b;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          b[r] = __builtin_amdgcn_perm(q.w[2 * r + 1][c >> 1], q.w[2 * r][c >> 1], (c & 1) ? 0x07060302u : 0x05040100u);
+        const bf16x8 wb = __builtin_bit_cast(bf16x8, b);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          if (t == 0 || t < nt) {
+#pragma unroll
+            for (int u = 0; u < PARTS; ++u)
+              acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, q.x[t][u]), wb, acc[t][c],
+                                                                  0, 0, 0);
+          }
+        }
+      }
+    };
+    if (cnt > 0) {
+      Step q0, q1;
+      load(0, q0);
+      load(cnt > 1 ? 1 : 0, q1);
+      int i = 0;
+      for (; i + 3 < cnt; i += 2) {
+        use(q0);
+        load(i + 2, q0);
+        use(q1);
+        load(i + 3, q1);
+      }
+      const int rest = cnt - i;  // 1..3
+      use(q0);
+      if (rest == 3) load(i + 2, q0);
+      if (rest >= 2) use(q1);
+      if (rest == 3) use(q0);
+    }
+    // acc[t][c] of lane 16 g + j: rows 4 g .. 4 g + 3 of tile t, column 8 j + c
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (t >= nt) break;
+      if (t > 0 || r0 > 0) __syncthreads();
+#pragma unroll
+      for (int c = 0; c < 8; ++c) sums[wave][c][lane] = acc[t][c];
+      __syncthreads();
+      // thread -> row 4 rg + ri of the tile and chunk q: neighbours read neighbouring words
+      for (int u = tid; u < 256; u += WAVES * 64) {
+        const int q = u & 15, ri = (u >> 4) & 3, rg = u >> 6;
+        const int r = r0 + t * 16 + rg * 4 + ri;
+        const float* s = (const float*)&sums[0][0][0] + (rg * 16 + q) * 4 + ri;
+        float v[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          float f = s[c * 256];
+#pragma unroll
+          for (int w = 1; w < WAVES; ++w) f += s[(w * 8 + c) * 256];
+          v[c] = f;
+        }
+        const bool live = r < n;
+        const int p = sh.row[live ? r : 0];
+        if (GATE && a.splits == 1) {
+          // chunk q < 8 is left, chunk q + 8, eight lanes on, its gate
+          uint16_t hi[8], lo[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float gate = __shfl_down(v[c], 8, 64);
+            const float hv = swg::swiglu_h(v[c], gate);
+            const bf16_t top = (bf16_t)hv;
+            const bf16_t low = (bf16_t)(hv - (float)top);
+            hi[c] = __builtin_bit_cast(uint16_t, top);
+            lo[c] = __builtin_bit_cast(uint16_t, low);
+          }
+          if (live && q < 8) {
+            uint16_t* hp = a.h + (int64_t)p * I + blockIdx.x * 64 + q * 8;
+            u32x4 vh, vl;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              vh[c] = hi[2 * c] | (uint32_t)hi[2 * c + 1] << 16;
+              vl[c] = lo[2 * c] | (uint32_t)lo[2 * c + 1] << 16;
+            }
+            *(u32x4*)hp = vh;
+            *(u32x4*)(hp + (int64_t)a.P * I) = vl;
+          }
+        } else if (live) {
+          int oc;
+          if constexpr (GATE) oc = blockIdx.x * 64 + (q & 7) * 8 + (q >> 3) * I;
+          else oc = blockIdx.x * 128 + q * 8;
+          if (GATE || oc < a.N) {
+            float* o = a.part + ((int64_t)blockIdx.z * a.P + p) * a.N + oc;
+            *(f32x4*)o = f32x4{v[0], v[1], v[2], v[3]};
+            *(f32x4*)(o + 4) = f32x4{v[4], v[5], v[6], v[7]};
+          }
+        }
+      }
+    }
+    if (r0 + 16 * NT < n) __syncthreads();
+  }
+}
+
+// h of the rows from the gate/up parts (where K was split), in two bf16 halves
+__global__ void __launch_bounds__(256) few_swiglu_kernel(const float* __restrict__ part, const int* __restrict__ ids,
+                                                         int splits, int P, int E, int I, uint16_t* __restrict__ h) {
+  const int64_t per = I / 8, t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (t >= P * per) return;
+  const int p = (int)(t / per), c0 = (int)(t % per) * 8;
+  if ((unsigned)ids[p] >= (unsigned)E) return;
+  float l[8] = {}, g[8] = {};
+  for (int s = 0; s < splits; ++s) {
+    const float* q = part + ((int64_t)s * P + p) * 2 * I + c0;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      l[c] += q[c];
+      g[c] += q[I + c];
+    }
+  }
+  uint16_t* hp = h + (int64_t)p * I + c0;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const float hv = swg::swiglu_h(l[c], g[c]);
+    const bf16_t top = (bf16_t)hv;
+    hp[c] = __builtin_bit_cast(uint16_t, top);
+    hp[(int64_t)P * I + c] = __builtin_bit_cast(uint16_t, (bf16_t)(hv - (float)top));
+  }
+}
+
+// y[m] = rn(sum over the choices j of weights[m,j] times the sum of the row's
+// parts).  A choice whose id names no expert adds nothing.
+__global__ void __launch_bounds__(256) few_combine_kernel(const float* __restrict__ part, const int* __restrict__ ids,
+                                                          const float* __restrict__ weights, int splits, int M, int E,
+                                                          int k, int N, uint16_t* __restrict__ y) {
+  const int64_t per = N / 4, t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (t >= M * per) return;
+  const int m = (int)(t / per), c0 = (int)(t % per) * 4;
+  f32x4 v = {};
+  for (int j = 0; j < k; ++j) {
+    const int p = m * k + j;
+    if ((unsigned)ids[p] >= (unsigned)E) continue;
+    f32x4 s = *(const f32x4*)(part + (int64_t)p * N + c0);
+    for (int q = 1; q < splits; ++q) s += *(const f32x4*)(part + ((int64_t)q * M * k + p) * N + c0);
+    const float w = weights[p];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = __builtin_fmaf(w, s[c], v[c]);
+  }
+  uint2 o;
+  o.x = swg::pack2(v[0], v[1]);
+  o.y = swg::pack2(v[2], v[3]);
+  *(uint2*)(y + (int64_t)m * N + c0) = o;
+}
+
+}  // namespace swb
+
+// ===========================================================================
+// Host side
+// ===========================================================================
+namespace {
+
+using namespace swb;
+
+constexpr int64_t kFewTokens = 64;
+constexpr int64_t kFewDim = (int64_t)1 << 20;
+constexpr int kUnits = 256;  // compute units of an MI355X
+constexpr int kWaves = 8;
+
+int64_t route_slices(int64_t D) { return (D + kRouteSlice - 1) / kRouteSlice; }
+
+// Parts of K: so many that the launch has a workgroup for every compute unit
+// when every slot has its expert, but at least a step of 32 for every wave.
+int few_splits(int64_t blocks, int64_t slots, int64_t K) {
+  int64_t s = kUnits / (blocks * slots);
+  const int64_t most = K / (32 * kWaves);
+  if (s > most) s = most;
+  return s < 1 ? 1 : (int)s;
+}
+
+struct Plan {
+  int64_t P, slots;
+  int s1, s2;                      // parts of D in the gate/up, of I in the down product
+  size_t route, h, part1, part2;   // bytes
+};
+
+Plan plan_few(int64_t M, int64_t D, int64_t I, int64_t Dout, int64_t E, int64_t k) {
+  Plan p{};
+  p.P = M * k;
+  p.slots = p.P < E ? p.P : E;
+  if (p.P == 0) return p;
+  p.s1 = few_splits(I / 64, p.slots, D);
+  p.s2 = few_splits((Dout + 127) / 128, p.slots, I);
+  p.h = align256((size_t)(2 * p.P * I * 2));
+  p.part1 = p.s1 > 1 ? align256((size_t)(p.s1 * p.P * 2 * I * 4)) : 0;
+  p.part2 = align256((size_t)(p.s2 * p.P * Dout * 4));
+  return p;
+}
+
+int check_few_dim(int64_t d) {
+  if (d <= 0) return SWIGLU_ERR_SHAPE;
+  return d % 64 != 0 || d > kFewDim ? SWIGLU_ERR_UNSUPPORTED : SWIGLU_OK;
+}
+int check_pairs(int64_t M, int64_t E, int64_t k) {
+  if (M < 0 || E < 1 || k < 1) return SWIGLU_ERR_SHAPE;
+  if (M > kFewTokens || E > kMaxExperts || k > 64 || M * k > kMaxPairs) return SWIGLU_ERR_UNSUPPORTED;
+  return SWIGLU_OK;
+}
+// a router's choice: k different experts
+int check_choice(int64_t M, int64_t E, int64_t k) {
+  SW_TRY(check_pairs(M, E, k));
+  return k > E ? SWIGLU_ERR_SHAPE : SWIGLU_OK;
+}
+int check_few(int64_t M, int64_t D, int64_t I, int64_t Dout, int64_t E, int64_t k) {
+  SW_TRY(check_pairs(M, E, k));
+  SW_TRY(check_few_dim(D));
+  SW_TRY(check_few_dim(I));
+  return check_few_dim(Dout);
+}
+
+size_t route_bytes(int64_t M, int64_t D, int64_t E) { return align256((size_t)(route_slices(D) * M * E * 8)); }
+
+int run_route(const void* x, const void* wr, int* ids, float* weights, void* ws, int64_t M, int64_t D, int64_t E,
+              int64_t k, int renorm, hipStream_t st) {
+  const int slices = (int)route_slices(D);
+  hipLaunchKernelGGL(route_logits_kernel,
+                     dim3((unsigned)slices, (unsigned)((M + kRouteTokens - 1) / kRouteTokens), (unsigned)((E + 255) / 256)),
+                     dim3(256), 0, st, (const uint16_t*)x, (const uint16_t*)wr, (double*)ws, (int)M, (int)D, (int)E);
+  SW_TRY(launch_status());
+  hipLaunchKernelGGL(route_topk_kernel, dim3((unsigned)M), dim3(64), 0, st, (const double*)ws, slices, (int)M, (int)E,
+                     (int)k, renorm, ids, weights);
+  return launch_status();
+}
+
+template <bool GATE>
+int run_few(const FewArgs& a, int64_t M, int64_t slots, hipStream_t st) {
+  const unsigned blocks = GATE ? (unsigned)(a.N / 128) : (unsigned)((a.N + 127) / 128);
+  const dim3 grid(blocks, (unsigned)slots, (unsigned)a.splits);
+  if (M <= 16) hipLaunchKernelGGL((few_kernel<1, kWaves, GATE>), grid, dim3(kWaves * 64), 0, st, a);
+  else if (M <= 32) hipLaunchKernelGGL((few_kernel<2, kWaves, GATE>), grid, dim3(kWaves * 64), 0, st, a);
+  else hipLaunchKernelGGL((few_kernel<4, kWaves, GATE>), grid, dim3(kWaves * 64), 0, st, a);
+  return launch_status();
+}
+
+int run_experts(const void* x, const void* W1, const void* W_down, const int* ids, const float* weights, void* y,
+                void* ws, const Plan& pl, int64_t M, int64_t D, int64_t I, int64_t Dout, int64_t E, int64_t k,
+                hipStream_t st) {
+  char* w = (char*)ws;
+  uint16_t* h = (uint16_t*)w;
+  float* part1 = (float*)(w + pl.h);
+  float* part2 = (float*)(w + pl.h + pl.part1);
+  FewArgs a{};
+  a.x = (const uint16_t*)x;
+  a.w = (const uint16_t*)W1;
+  a.ids = ids;
+  a.part = part1;
+  a.h = h;
+  a.P = (int)pl.P;
+  a.E = (int)E;
+  a.k = (int)k;
+  a.K = (int)D;
+  a.N = (int)(2 * I);
+  a.splits = pl.s1;
+  SW_TRY(run_few<true>(a, M, pl.slots, st));
+  if (pl.s1 > 1) {
+    hipLaunchKernelGGL(few_swiglu_kernel, dim3((unsigned)((pl.P * (I / 8) + 255) / 256)), dim3(256), 0, st,
+                       (const float*)part1, ids, pl.s1, (int)pl.P, (int)E, (int)I, h);
+    SW_TRY(launch_status());
+  }
+  a.x = h;
+  a.w = (const uint16_t*)W_down;
+  a.part = part2;
+  a.h = nullptr;
+  a.K = (int)I;
+  a.N = (int)Dout;
+  a.splits = pl.s2;
+  SW_TRY(run_few<false>(a, M, pl.slots, st));
+  hipLaunchKernelGGL(few_combine_kernel, dim3((unsigned)((M * (Dout / 4) + 255) / 256)), dim3(256), 0, st,
+                     (const float*)part2, ids, weights, pl.s2, (int)M, (int)E, (int)k, (int)Dout, (uint16_t*)y);
+  return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t swiglu_moe_route_workspace(int64_t M, int64_t D, int64_t E, int64_t k) {
+  if (check_choice(M, E, k) != SWIGLU_OK || check_few_dim(D) != SWIGLU_OK) return 0;
+  return route_bytes(M, D, E);
+}
+
+int swiglu_moe_route(const void* x, const void* W_router, int32_t* ids, float* weights, void* ws, size_t ws_bytes,
+                     int64_t M, int64_t D, int64_t E, int64_t k, int renormalize, void* stream) {
+  SW_TRY(check_choice(M, E, k));
+  SW_TRY(check_few_dim(D));
+  if (!W_router || (M > 0 && (!x || !ids || !weights))) return SWIGLU_ERR_NULL;
+  if (!aligned_to(x, 2) || !aligned_to(W_router, 2) || !aligned_to(ids, 4) || !aligned_to(weights, 4) ||
+      !aligned_to(ws, 16))
+    return SWIGLU_ERR_ALIGN;
+  const size_t need = route_bytes(M, D, E);
+  if (need > 0 && (!ws || ws_bytes < need)) return SWIGLU_ERR_WORKSPACE;
+  const Range ins[] = {rng(x, M * D * 2), rng(W_router, D * E * 2)};
+  const Range outs[] = {rng(ids, M * k * 4), rng(weights, M * k * 4), rng(ws, (int64_t)need)};
+  SW_TRY(check_alias(ins, 2, outs, 3));
+  if (M == 0) return SWIGLU_OK;
+  return run_route(x, W_router, ids, weights, ws, M, D, E, k, renormalize ? 1 : 0, as_stream(stream));
+}
+
+// h, the gate/up parts, the down parts
+size_t swiglu_moe_few_workspace(int64_t M, int64_t D, int64_t I, int64_t Dout, int64_t E, int64_t k) {
+  if (check_few(M, D, I, Dout, E, k) != SWIGLU_OK) return 0;
+  const Plan p = plan_few(M, D, I, Dout, E, k);
+  return p.h + p.part1 + p.part2;
+}
+
+int swiglu_moe_few_fwd(const void* x, const void* W1, const void* W_down, const int32_t* ids, const float* weights,
+                       void* y, void* ws, size_t ws_bytes, int64_t M, int64_t D, int64_t I, int64_t Dout, int64_t E,
+                       int64_t k, void* stream) {
+  SW_TRY(check_few(M, D, I, Dout, E, k));
+  if (!W1 || !W_down || (M > 0 && (!x || !ids || !weights || !y))) return SWIGLU_ERR_NULL;
+  if (!aligned_to(x, 16) || !aligned_to(W1, 16) || !aligned_to(W_down, 16) || !aligned_to(ids, 4) ||
+      !aligned_to(weights, 4) || !aligned_to(y, 16) || !aligned_to(ws, 16))
+    return SWIGLU_ERR_ALIGN;
+  const Plan pl = plan_few(M, D, I, Dout, E, k);
+  const size_t need = pl.h + pl.part1 + pl.part2;
+  if (need > 0 && (!ws || ws_bytes < need)) return SWIGLU_ERR_WORKSPACE;
+  const Range ins[] = {rng(x, M * D * 2), rng(W1, E * D * 2 * I * 2), rng(W_down, E * I * Dout * 2),
+                       rng(ids, M * k * 4), rng(weights, M * k * 4)};
+  const Range outs[] = {rng(y, M * Dout * 2), rng(ws, (int64_t)need)};
+  SW_TRY(check_alias(ins, 5, outs, 2));
+  if (M == 0) return SWIGLU_OK;
+  return run_experts(x, W1, W_down, ids, weights, y, ws, pl, M, D, I, Dout, E, k, as_stream(stream));
+}
+
+size_t swiglu_moe_few_layer_workspace(int64_t M, int64_t D, int64_t I, int64_t Dout, int64_t E, int64_t k) {
+  if (check_few(M, D, I, Dout, E, k) != SWIGLU_OK || check_choice(M, E, k) != SWIGLU_OK) return 0;
+  return swiglu_moe_few_workspace(M, D, I, Dout, E, k) + route_bytes(M, D, E);
+}
+
+int swiglu_moe_few_layer(const void* x, const void* W_router, const void* W1, const void* W_down, void* y,
+                         int32_t* ids, float* weights, void* ws, size_t ws_bytes, int64_t M, int64_t D, int64_t I,
+                         int64_t Dout, int64_t E, int64_t k, int renormalize, void* stream) {
+  SW_TRY(check_few(M, D, I, Dout, E, k));
+  SW_TRY(check_choice(M, E, k));
+  if (!W_router || !W1 || !W_down || (M > 0 && (!x || !ids || !weights || !y))) return SWIGLU_ERR_NULL;
+  if (!aligned_to(x, 16) || !aligned_to(W_router, 2) || !aligned_to(W1, 16) || !aligned_to(W_down, 16) ||
+      !aligned_to(ids, 4) || !aligned_to(weights, 4) || !aligned_to(y, 16) || !aligned_to(ws, 16))
+    return SWIGLU_ERR_ALIGN;
+  const Plan pl = plan_few(M, D, I, Dout, E, k);
+  const size_t own = pl.h + pl.part1 + pl.part2, need = own + route_bytes(M, D, E);
+  if (need > 0 && (!ws || ws_bytes < need)) return SWIGLU_ERR_WORKSPACE;
+  const Range ins[] = {rng(x, M * D * 2), rng(W_router, D * E * 2), rng(W1, E * D * 2 * I * 2),
+                       rng(W_down, E * I * Dout * 2)};
+  const Range outs[] = {rng(y, M * Dout * 2), rng(ids, M * k * 4), rng(weights, M * k * 4), rng(ws, (int64_t)need)};
+  SW_TRY(check_alias(ins, 4, outs, 4));
+  if (M == 0) return SWIGLU_OK;
+  hipStream_t st = as_stream(stream);
+  SW_TRY(run_route(x, W_router, ids, weights, (char*)ws + own, M, D, E, k, renormalize ? 1 : 0, st));
+  return run_experts(x, W1, W_down, ids, weights, y, ws, pl, M, D, I, Dout, E, k, st);
+}
+
+}  // extern "C"

@@ -2,7 +2,8 @@
  * swiglu_block.h -- C ABI of the operators around the SwiGLU MLP step
  * (swiglu_mlp.h) in a block that trains or serves it, on MI355X (gfx950):
  *   - layer norm, forward and backward (in front of the MLP);
- *   - the global gradient norm and clipping (behind the backward).
+ *   - the global gradient norm and clipping (behind the backward);
+ *   - a whole mixture-of-experts layer for a few tokens (serving).
  *
  * Conventions, where they are not those of swiglu_mlp.h:
  *   - Element types are passed as a swiglu_dtype.  Sums, statistics and
@@ -82,6 +83,44 @@ size_t swiglu_clip_grad_norm_workspace(int64_t n);
  * infinity: the norm alone (outs must be NULL or in place). */
 int swiglu_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes,
                           int64_t n, double max_norm, float* total, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * A mixture-of-experts layer for a few tokens (decoding): the router, and the
+ * expert MLPs of swiglu_moe_fwd without packed rows.  bf16 tensors, row-major
+ * and densely packed; 0 <= M <= 64 tokens, 1 <= E <= 1024 experts,
+ * 1 <= k <= 64 choices of a token (k <= E where the router makes them),
+ * M * k <= 1024; D, I and Dout are positive multiples of 64 up to 2^20.  x, W1,
+ * W_down and y are 16-byte aligned.
+ *   W_router [D,E], W1 [E,D,2I] ([left | gate]), W_down [E,I,Dout]
+ *   ids int32 [M,k], weights float [M,k]
+ * ------------------------------------------------------------------------- */
+
+/* ids[m] = the k experts with the largest logits x[m] . W_router, the largest
+ * first, equal ones in order of their number; weights = their softmax over all
+ * E logits, divided by the k weights' sum if renormalize.  The logits are sums
+ * in 64 bits, so that the choice does not depend on an order of summation.  A
+ * NaN logit orders as the lowest and makes its token's weights NaN. */
+size_t swiglu_moe_route_workspace(int64_t M, int64_t D, int64_t E, int64_t k);
+int swiglu_moe_route(const void* x, const void* W_router, int32_t* ids, float* weights,
+                     void* ws, size_t ws_bytes,
+                     int64_t M, int64_t D, int64_t E, int64_t k, int renormalize, void* stream);
+
+/* y[m] = sum_j weights[m,j] MLP_{ids[m,j]}(x[m]), rounded once: the
+ * pre-activations are held in 32 bits, h in 16 significant bits, the sum over j
+ * in 32.  An id outside [0, E) adds nothing (a token with no other gets
+ * zeros); a token may name an expert more than once.  Only the experts that
+ * are named are read. */
+size_t swiglu_moe_few_workspace(int64_t M, int64_t D, int64_t I, int64_t Dout, int64_t E, int64_t k);
+int swiglu_moe_few_fwd(const void* x, const void* W1, const void* W_down, const int32_t* ids, const float* weights,
+                       void* y, void* ws, size_t ws_bytes,
+                       int64_t M, int64_t D, int64_t I, int64_t Dout, int64_t E, int64_t k, void* stream);
+
+/* Both in one call: writes y [M,Dout], ids and weights. */
+size_t swiglu_moe_few_layer_workspace(int64_t M, int64_t D, int64_t I, int64_t Dout, int64_t E, int64_t k);
+int swiglu_moe_few_layer(const void* x, const void* W_router, const void* W1, const void* W_down,
+                         void* y, int32_t* ids, float* weights, void* ws, size_t ws_bytes,
+                         int64_t M, int64_t D, int64_t I, int64_t Dout, int64_t E, int64_t k, int renormalize,
+                         void* stream);
 
 #ifdef __cplusplus
 }

@@ -130,3 +130,64 @@ def test_clip_binding_refuses_host_tensors_and_nothing():
         sw.swiglu_clip_grad_norm([None], 1.0)
     with pytest.raises(ValueError):
         sw.swiglu_grad_norm(torch.zeros(4))
+
+
+def test_moe_route_refuses():
+    L = sw.lib()
+
+    def f(p=None, wsb=1 << 30, M=4, D=64, E=8, k=2):
+        q = [addr(i) for i in range(5)]      # x W_router ids weights ws
+        for i, v in (p or {}).items():
+            q[i] = v
+        return L.swiglu_moe_route(*q, wsb, M, D, E, k, 1, None)
+    assert f(M=-1) == SHAPE and f(E=0) == SHAPE and f(k=0) == SHAPE and f(k=9) == SHAPE and f(D=0) == SHAPE
+    assert f(M=65) == UNSUP and f(E=1025) == UNSUP and f(E=100, k=65) == UNSUP and f(M=64, E=64, k=17) == UNSUP
+    assert f(D=100) == UNSUP and f(D=1 << 21) == UNSUP
+    for i in range(4):
+        assert f({i: None}) == NULL, i
+    assert f({0: addr(0) + 1}) == ALIGN and f({2: addr(2) + 2}) == ALIGN and f({4: addr(4) + 8}) == ALIGN
+    need = L.swiglu_moe_route_workspace(4, 64, 8, 2)
+    assert need > 0 and f(wsb=need - 1) == WS and f({4: None}) == WS
+    assert f({2: addr(3)}) == ALIAS and f({2: addr(0) + 64}) == ALIAS and f({4: addr(1)}) == ALIAS
+    assert L.swiglu_moe_route_workspace(4, 100, 8, 2) == 0 and L.swiglu_moe_route_workspace(4, 64, 8, 9) == 0
+    assert f({0: None, 2: None, 3: None}, M=0) == OK
+
+
+def test_moe_few_refuses():
+    L = sw.lib()
+
+    def few(p=None, wsb=1 << 40, M=4, D=64, I=128, Dout=192, E=8, k=2):
+        q = [addr(i) for i in range(7)]      # x W1 W_down ids weights y ws
+        for i, v in (p or {}).items():
+            q[i] = v
+        return L.swiglu_moe_few_fwd(*q, wsb, M, D, I, Dout, E, k, None)
+
+    def layer(p=None, wsb=1 << 40, M=4, D=64, I=128, Dout=192, E=8, k=2):
+        q = [addr(i) for i in range(8)]      # x W_router W1 W_down y ids weights ws
+        for i, v in (p or {}).items():
+            q[i] = v
+        return L.swiglu_moe_few_layer(*q, wsb, M, D, I, Dout, E, k, 1, None)
+    for f, last in ((few, 6), (layer, 7)):
+        assert f(M=-1) == SHAPE and f(E=0) == SHAPE and f(k=0) == SHAPE and f(I=0) == SHAPE and f(Dout=-64) == SHAPE
+        assert f(E=100, k=65) == UNSUP and f(M=64, E=20, k=17) == UNSUP
+        assert f(M=65) == UNSUP and f(I=96) == UNSUP and f(Dout=100) == UNSUP and f(D=(1 << 20) + 64) == UNSUP
+        for i in range(last):
+            assert f({i: None}) == NULL, i
+        assert f({0: addr(0) + 2}) == ALIGN and f({last: addr(last) + 8}) == ALIGN
+        assert f({last: None}) == WS and f(wsb=100) == WS
+    assert layer(k=9) == SHAPE                       # the router cannot choose more than there are
+    dims = (4, 64, 128, 192, 8, 2)
+    assert few(wsb=L.swiglu_moe_few_workspace(*dims) - 1) == WS
+    assert layer(wsb=L.swiglu_moe_few_layer_workspace(*dims) - 1) == WS
+    assert L.swiglu_moe_few_workspace(4, 64, 100, 192, 8, 2) == 0
+    assert few({5: addr(0)}) == ALIAS and few({5: addr(3)}) == ALIAS and few({6: addr(1) + (1 << 16)}) == ALIAS
+    assert layer({4: addr(0)}) == ALIAS and layer({5: addr(6)}) == ALIAS and layer({7: addr(2)}) == ALIAS
+    assert few({0: None, 3: None, 4: None, 5: None}, M=0) == OK
+
+
+def test_moe_few_binding_refuses_host_tensors():
+    z = torch.zeros(2, 64, dtype=torch.bfloat16)
+    for f in (lambda: sw.swiglu_moe_route(z, z, 1), lambda: sw.swiglu_moe_few_fwd(z, z, z, z, z),
+              lambda: sw.swiglu_moe_few_layer(z, z, z, z, 1)):
+        with pytest.raises(ValueError):
+            f()

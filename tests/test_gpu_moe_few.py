@@ -1,0 +1,270 @@
+"""The mixture-of-experts layer for a few tokens against the definition in 64
+bits.
+
+Tolerances.  e = 2^-24.  A pre-activation is the sum of D products, an eighth
+of them in one chain, then eight sums: within (D / 8 + 16) e of the sum of the
+products' magnitudes.  h = left silu(gate): the two errors through its partial
+derivatives (|silu'| < 1.1), the activation's own (exponential and reciprocal
+of the hardware, 1 ulp each, and the exponent's rounding, |gate| e): (8 +
+|gate|) e, and the two halves it is held in, 2^-17.  A result is a sum of I
+products in the same way, a weighted sum over k choices, and one rounding to
+bf16, 2^-8 of half a step."""
+import pytest
+import torch
+
+import bwd_gemm_epilogue_amd as sw
+
+pytestmark = pytest.mark.gpu
+
+E32 = 2.0 ** -24
+U = torch.finfo(torch.bfloat16).eps / 2
+
+
+def make(M, D, I, Dout, E, seed=0, gate_scale=1.0):
+    g = torch.Generator().manual_seed(seed + 1000 * M + D + I)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    bf = torch.bfloat16
+    W1 = r(E, D, 2 * I) * D ** -0.5
+    W1[..., I:] *= gate_scale
+    return r(M, D).to(bf), (r(D, E) * D ** -0.5).to(bf), W1.to(bf), (r(E, I, Dout) * I ** -0.5).to(bf)
+
+
+def route64(x, Wr, k, renorm):
+    """ids and weights from 64-bit logits; equal logits in order of their number"""
+    l = x.double() @ Wr.double()
+    ids = torch.sort(l, dim=1, descending=True, stable=True).indices[:, :k]
+    w = torch.gather(torch.softmax(l, 1), 1, ids)
+    return ids, w / w.sum(1, keepdim=True) if renorm else w
+
+
+def layer64(x, W1, Wd, ids, weights):
+    """(y, tolerance) for given ids and weights"""
+    M, D = x.shape
+    E, I, Dout = Wd.shape
+    y, tol = (torch.zeros(M, Dout, dtype=torch.float64) for _ in range(2))
+    k1, k2 = (D / 8 + 16) * E32, (I / 8 + 16 + ids.shape[1]) * E32
+    for m in range(M):
+        for j in range(ids.shape[1]):
+            e, w = int(ids[m, j]), float(weights[m, j])
+            if not 0 <= e < E:
+                continue
+            xm, w1, wd = x[m].double(), W1[e].double(), Wd[e].double()
+            pre, mag = xm @ w1, xm.abs() @ w1.abs()
+            left, gate = pre[:I], pre[I:]
+            silu = gate * torch.sigmoid(gate)
+            h = left * silu
+            dh = silu.abs() * k1 * mag[:I] + 1.1 * left.abs() * k1 * mag[I:] + h.abs() * ((8 + gate.abs()) * E32 + 2.0 ** -17)
+            y[m] += w * (h @ wd)
+            tol[m] += abs(w) * (dh @ wd.abs() + k2 * (h.abs() @ wd.abs()))
+    return y, tol + U * y.abs() + 1e-38
+
+
+def check(got, x, W1, Wd, ids, weights):
+    y, tol = layer64(x, W1, Wd, ids, weights)
+    d = (got.cpu().double() - y).abs()
+    assert got.dtype == torch.bfloat16 and (d <= tol).all(), float((d / tol).max())
+
+
+CASES = [  # M D I Dout E k
+    (1, 64, 64, 64, 1, 1), (1, 128, 64, 192, 4, 2), (2, 64, 128, 64, 3, 3), (3, 320, 192, 320, 7, 2), (1, 1024, 512, 256, 60, 6),
+    (5, 192, 64, 128, 60, 6), (16, 256, 128, 256, 8, 2), (17, 64, 192, 64, 2, 1), (31, 128, 64, 128, 4, 4), (33, 192, 128, 64, 2, 2),
+    (48, 64, 64, 192, 16, 8), (64, 128, 128, 128, 4, 4), (64, 64, 64, 64, 64, 16), (7, 64, 64, 64, 300, 8), (4, 128, 64, 64, 1024, 64),
+    (1, 2048, 1024, 2048, 4, 2), (6, 576, 704, 448, 5, 3),
+]
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("c", CASES, ids=lambda c: "x".join(map(str, c)))
+def test_layer(c, renorm):
+    M, D, I, Dout, E, k = c
+    x, Wr, W1, Wd = make(M, D, I, Dout, E)
+    y, ids, weights = sw.swiglu_moe_few_layer(x.cuda(), Wr.cuda(), W1.cuda(), Wd.cuda(), k, renormalize=renorm)
+    rid, rw = route64(x, Wr, k, renorm)
+    assert ids.dtype == torch.int32 and torch.equal(ids.cpu().long(), rid)
+    # the softmax in 64 bits (its own function there), rounded once
+    assert ((weights.cpu().double() - rw).abs() <= 1.001 * E32 * rw + 1e-45).all()
+    check(y, x, W1, Wd, rid, weights.cpu())
+    # the two halves give the same bits
+    i2, w2 = sw.swiglu_moe_route(x.cuda(), Wr.cuda(), k, renormalize=renorm)
+    assert torch.equal(i2, ids) and torch.equal(w2, weights)
+    assert torch.equal(sw.swiglu_moe_few_fwd(x.cuda(), W1.cuda(), Wd.cuda(), ids, weights), y)
+
+
+def test_saturated_gates():
+    x, Wr, W1, Wd = make(9, 256, 128, 128, 4, gate_scale=8.0)
+    y, ids, weights = sw.swiglu_moe_few_layer(x.cuda(), Wr.cuda(), W1.cuda(), Wd.cuda(), 2)
+    check(y, x, W1, Wd, ids.cpu(), weights.cpu())
+
+
+@pytest.mark.parametrize("M,k", [(1, 1), (16, 1), (40, 1), (64, 4), (64, 16)])
+def test_every_choice_names_one_expert(M, k):
+    """Up to 1024 rows of one expert, tokens that name it more than once."""
+    x, _, W1, Wd = make(M, 128, 64, 64, 3)
+    ids = torch.full((M, k), 1, dtype=torch.int32)
+    w = torch.randn(M, k, generator=torch.Generator().manual_seed(M))
+    W1[[0, 2]], Wd[[0, 2]] = float("nan"), float("nan")   # never read
+    y = sw.swiglu_moe_few_fwd(x.cuda(), W1.cuda(), Wd.cuda(), ids.cuda(), w.cuda())
+    check(y, x, W1, Wd, ids, w)
+
+
+def test_ids_that_name_no_expert():
+    M, E, k = 12, 5, 3
+    x, _, W1, Wd = make(M, 64, 64, 128, E)
+    g = torch.Generator().manual_seed(4)
+    ids = torch.randint(0, E, (M, k), generator=g, dtype=torch.int32)
+    w = torch.rand(M, k, generator=g)
+    ids[0] = -1                                      # a token with no expert: zeros
+    ids[1] = torch.tensor([E, -5, 2 ** 31 - 1], dtype=torch.int32)
+    ids[2, 1] = E + 7
+    ids[3, 0], w[3, 0] = -1, float("nan")            # its weight does not count either
+    ws = torch.full((sw.swiglu_moe_few_workspace(M, 64, 64, 128, E, k),), 255, dtype=torch.uint8, device="cuda")
+    y = sw.swiglu_moe_few_fwd(x.cuda(), W1.cuda(), Wd.cuda(), ids.cuda(), w.cuda(), ws=ws)
+    check(y, x, W1, Wd, ids, w)
+    assert not y[0].any() and not y[1].any()
+    none = sw.swiglu_moe_few_fwd(x.cuda(), W1.cuda(), Wd.cuda(), torch.full_like(ids, -1).cuda(), w.cuda())
+    assert not none.any()
+
+
+def test_equal_logits_go_to_the_lowest_number():
+    x, Wr, _, _ = make(20, 192, 64, 64, 1)
+    for E, k in ((9, 4), (70, 7), (300, 10)):
+        Wr = torch.randn(192, 3, generator=torch.Generator().manual_seed(E)).to(torch.bfloat16)
+        Wr = Wr[:, torch.arange(E) % 3].contiguous()      # every third column the same
+        ids, w = sw.swiglu_moe_route(x.cuda(), Wr.cuda(), k)
+        rid, rw = route64(x, Wr, k, True)
+        assert torch.equal(ids.cpu().long(), rid)
+        assert ((w.cpu().double() - rw).abs() <= 1.001 * E32 * rw).all()
+    ids, w = sw.swiglu_moe_route(torch.zeros_like(x).cuda(), Wr.cuda(), 5)
+    assert torch.equal(ids.cpu(), torch.arange(5, dtype=torch.int32).expand(20, 5)) and (w == 0.2).all()
+
+
+def test_infinite_and_nan_tokens_stay_theirs():
+    x, Wr, W1, Wd = make(6, 128, 64, 64, 10)
+    args = [v.cuda() for v in (Wr, W1, Wd)]
+    clean = sw.swiglu_moe_few_layer(x.cuda(), *args, 3)
+    x2 = x.clone()
+    x2[1, 5], x2[4, 0] = float("nan"), float("inf")
+    y, ids, w = sw.swiglu_moe_few_layer(x2.cuda(), *args, 3)
+    keep = [0, 2, 3, 5]
+    for a, b in zip((y, ids, w), clean):
+        assert torch.equal(a[keep], b[keep])
+    assert ((ids >= 0) & (ids < 10)).all()
+    assert w[1].isnan().all() and w[4].isnan().all() and y[1].isnan().all() and y[4].isnan().all()
+
+
+def test_large_logits_and_minus_infinity():
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    x[:, 0] = 1.0
+    Wr = torch.zeros(64, 6, dtype=torch.bfloat16)
+    Wr[0] = torch.tensor([-300.0, 200.0, float("-inf"), 200.0, 199.0, float("-inf")])
+    ids, w = sw.swiglu_moe_route(x.cuda()[:, :], Wr.cuda(), 6, renormalize=False)
+    # 0 * -inf in no other row: the other inputs are zeros times finite weights
+    assert ids[0].tolist() == [1, 3, 4, 0, 2, 5]
+    e = 1 / (2 + torch.exp(torch.tensor(-1.0, dtype=torch.float64)))
+    assert abs(float(w[0, 0]) - float(e)) <= 1.001 * E32 and float(w[0, 4]) == 0.0 and float(w[0, 5]) == 0.0
+
+
+def test_no_tokens():
+    x, Wr, W1, Wd = make(1, 64, 64, 128, 3)
+    y, ids, w = sw.swiglu_moe_few_layer(x[:0].cuda(), Wr.cuda(), W1.cuda(), Wd.cuda(), 2)
+    assert y.shape == (0, 128) and ids.shape == w.shape == (0, 2)
+
+
+def test_offsets_past_32_bits():
+    """600 experts of 4 M weights: the last one's start lies past 2^31 elements."""
+    E, D, I, Dout = 600, 1024, 2048, 64
+    x, _, W1, Wd = make(2, D, I, Dout, 1)
+    big1 = torch.empty(E, D, 2 * I, dtype=torch.bfloat16, device="cuda")
+    bigd = torch.empty(E, I, Dout, dtype=torch.bfloat16, device="cuda")
+    big1[E - 1], bigd[E - 1] = W1[0].cuda(), Wd[0].cuda()
+    ids = torch.tensor([[E - 1], [E - 1]], dtype=torch.int32)
+    w = torch.tensor([[0.5], [2.0]])
+    y = sw.swiglu_moe_few_fwd(x.cuda(), big1, bigd, ids.cuda(), w.cuda())
+    check(y, x, W1, Wd, torch.zeros_like(ids), w)
+
+
+def test_writes_stay_in_their_tensors():
+    M, D, I, Dout, E, k = 5, 128, 192, 320, 6, 2
+    x, Wr, W1, Wd = make(M, D, I, Dout, E)
+    args = [v.cuda() for v in (x, Wr, W1, Wd)]
+    want = sw.swiglu_moe_few_layer(*args, k)
+
+    def guarded(shape, dtype, pad=64):
+        n = 1
+        for s in shape:
+            n *= s
+        buf = torch.full((n + pad,), 77, dtype=dtype, device="cuda")
+        return buf, buf[:n].view(shape)
+    yb, y = guarded((M, Dout), torch.bfloat16)
+    ib, ids = guarded((M, k), torch.int32)
+    wb, w = guarded((M, k), torch.float32)
+    sb, ws = guarded((sw.swiglu_moe_few_layer_workspace(M, D, I, Dout, E, k),), torch.uint8, 4096)
+    got = sw.swiglu_moe_few_layer(*args, k, y=y, ids=ids, weights=w, ws=ws)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    for buf, t in ((yb, y), (ib, ids), (wb, w), (sb, ws)):
+        assert (buf[t.numel():] == 77).all()
+
+
+def test_same_bits_every_time_and_on_another_stream():
+    x, Wr, W1, Wd = (v.cuda() for v in make(23, 256, 128, 256, 12))
+    first = sw.swiglu_moe_few_layer(x, Wr, W1, Wd, 4)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        again = sw.swiglu_moe_few_layer(x, Wr, W1, Wd, 4, stream=s)
+        s.synchronize()
+        for a, b in zip(first, again):
+            assert torch.equal(a, b)
+
+
+def test_in_a_graph():
+    x, Wr, W1, Wd = make(3, 256, 128, 256, 12)
+    X, rest = x.cuda(), [v.cuda() for v in (Wr, W1, Wd)]
+    sw.swiglu_moe_few_layer(X, *rest, 4)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        got = sw.swiglu_moe_few_layer(X, *rest, 4)
+    for k in range(4):
+        X.copy_(make(3, 256, 128, 256, 12, seed=k + 1)[0])
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, sw.swiglu_moe_few_layer(X, *rest, 4)):
+            assert torch.equal(a, b)
+
+
+def test_agrees_with_the_grouped_call_on_packed_rows():
+    """The same experts through swiglu_moe_fwd: bf16 storage of preact and h
+    there, so within a few bf16 roundings of the largest value."""
+    M, D, I, E, k = 24, 256, 128, 6, 2
+    x, Wr, W1, Wd = make(M, D, I, D, E)
+    y, ids, w = sw.swiglu_moe_few_layer(x.cuda(), Wr.cuda(), W1.cuda(), Wd.cuda(), k)
+    flat = ids.reshape(-1).long()
+    order = torch.argsort(flat, stable=True)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[1:] = torch.bincount(flat, minlength=E).cumsum(0)
+    packed = x.cuda().repeat_interleave(k, 0)[order].contiguous()
+    _, out = sw.swiglu_moe_fwd(packed, W1.cuda(), Wd.cuda(), off)
+    rows = torch.empty(M * k, D, device="cuda")
+    rows[order] = out.float()
+    ref = (rows.reshape(M, k, D) * w[..., None]).sum(1)
+    assert float((y.float() - ref).abs().max() / ref.abs().max()) <= 1e-2
+
+
+def test_refusals_on_the_gpu():
+    x, Wr, W1, Wd = (v.cuda() for v in make(4, 64, 64, 64, 3))
+    ids, w = sw.swiglu_moe_route(x, Wr, 2)
+    for bad in (lambda: sw.swiglu_moe_few_fwd(x, W1, Wd, ids.long(), w), lambda: sw.swiglu_moe_few_fwd(x, W1, Wd, ids, w.half()),
+                lambda: sw.swiglu_moe_few_fwd(x, W1, Wd, ids[:3], w), lambda: sw.swiglu_moe_few_fwd(x, W1[:2], Wd, ids, w),
+                lambda: sw.swiglu_moe_few_fwd(x, W1.cpu(), Wd, ids, w), lambda: sw.swiglu_moe_few_fwd(x.float(), W1, Wd, ids, w),
+                lambda: sw.swiglu_moe_few_fwd(x, W1[0], Wd, ids, w), lambda: sw.swiglu_moe_route(x, Wr[:32], 2),
+                lambda: sw.swiglu_moe_few_fwd(x.t(), W1, Wd, ids, w), lambda: sw.swiglu_moe_route(x[0], Wr, 2)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: sw.swiglu_moe_route(x, Wr, 4), lambda: sw.swiglu_moe_route(x, Wr, 0),
+                lambda: sw.swiglu_moe_few_layer(x.repeat(17, 1), Wr, W1, Wd, 2)):
+        with pytest.raises(sw.SwiGLUError):
+            bad()
