@@ -29,50 +29,43 @@ constexpr int kMaxPairs = 1024, kMaxExperts = 1024;
 // ---------------------------------------------------------------------------
 // Router
 // ---------------------------------------------------------------------------
-constexpr int kRouteTokens = 16;  // tokens of one workgroup
-constexpr int kRouteSlice = 128;  // rows of Wr of one workgroup
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+constexpr int kRouteSlice = 64;  // rows of Wr of one wave; D is a multiple
 
-// part[slice][m][e] = sum over the slice's d of x[m,d] Wr[d,e] in 64 bits: a
+__device__ __forceinline__ double bf16_f64(uint32_t bits) { return (double)swg::bf16_lo(bits); }
+
+// part[m][slice][e] = sum over the slice's d of x[m,d] Wr[d,e] in 64 bits: a
 // product of two bf16 values is exact there, and the sum is off by 2^-53 a term.
-// Thread t takes expert blockIdx.z * 256 + t % ew and every (256 / ew)-th row.
-__global__ void __launch_bounds__(256) route_logits_kernel(const uint16_t* __restrict__ x,
-                                                           const uint16_t* __restrict__ wr, double* __restrict__ part,
-                                                           int M, int D, int E) {
-  __shared__ double xs[kRouteSlice][kRouteTokens];
-  __shared__ double sums[256];
-  const int tid = threadIdx.x;
-  const int d0 = blockIdx.x * kRouteSlice, nd = min(kRouteSlice, D - d0);
-  const int m0 = blockIdx.y * kRouteTokens, nm = min(kRouteTokens, M - m0);
-  const int e0 = blockIdx.z * 256, ew = min(256, E - e0), rows = 256 / ew;
-  for (int i = tid; i < kRouteSlice * kRouteTokens; i += 256) {
-    const int m = i / kRouteSlice, d = i % kRouteSlice;
-    double v = 0.0;
-    if (m < nm && d < nd) v = (double)swg::bf16_lo(x[(int64_t)(m0 + m) * D + d0 + d]);
-    xs[d][m] = v;
-  }
-  __syncthreads();
-  const int r = tid / ew, e = tid - r * ew;
-  double acc[kRouteTokens];
+// One wave: 16 tokens, 16 experts, 64 d, sixteen v_mfma_f64_16x16x4.  Lane 16 g +
+// j holds token j's and expert j's values at d = 8 g + i (and 32 + 8 g + i) in
+// step i, so a token's eight are one load.
+__global__ void __launch_bounds__(64) route_logits_kernel(const uint16_t* __restrict__ x,
+                                                          const uint16_t* __restrict__ wr, double* __restrict__ part,
+                                                          int M, int D, int E) {
+  const int lane = threadIdx.x, j = lane & 15, g = lane >> 4;
+  const int d0 = blockIdx.x * kRouteSlice, m0 = blockIdx.y * 16, e0 = blockIdx.z * 16;
+  const uint16_t* xp = x + (int64_t)min(m0 + j, M - 1) * D + d0 + g * 8;
+  const uint16_t* wp = wr + (int64_t)(d0 + g * 8) * E + min(e0 + j, E - 1);
+  uint16_t xv[2][8], wv[2][8];
 #pragma unroll
-  for (int m = 0; m < kRouteTokens; ++m) acc[m] = 0.0;
-  if (r < rows) {
-    for (int d = r; d < nd; d += rows) {
-      const double w = (double)swg::bf16_lo(wr[(int64_t)(d0 + d) * E + e0 + e]);
+  for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int m = 0; m < kRouteTokens; ++m) acc[m] = __builtin_fma(xs[d][m], w, acc[m]);
+    for (int i = 0; i < 8; ++i) {
+      xv[h][i] = xp[h * 32 + i];
+      wv[h][i] = wp[(int64_t)(h * 32 + i) * E];
     }
   }
-  for (int m = 0; m < nm; ++m) {
-    double a = 0.0;
+  f64x4 acc = {};
 #pragma unroll
-    for (int q = 0; q < kRouteTokens; ++q) a = q == m ? acc[q] : a;
-    if (r < rows) sums[tid] = a;
-    __syncthreads();
-    if (r == 0) {
-      for (int q = 1; q < rows; ++q) a += sums[q * ew + e];
-      part[((int64_t)blockIdx.x * M + m0 + m) * E + e0 + e] = a;
-    }
-    __syncthreads();
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      acc = __builtin_amdgcn_mfma_f64_16x16x4f64(bf16_f64(xv[h][i]), bf16_f64(wv[h][i]), acc, 0, 0, 0);
+  // acc[r]: token 4 r + g, expert j
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int m = m0 + 4 * r + g;
+    if (m < M && e0 + j < E) part[((int64_t)m * gridDim.x + blockIdx.x) * E + e0 + j] = acc[r];
   }
 }
 
@@ -83,77 +76,87 @@ __device__ __forceinline__ double shfl_xor_f64(double v, int d) {
   return __builtin_bit_cast(double, b);
 }
 
-// One wave to a token.  Lane i holds experts i, i + 64, ...: the logits (the
-// slices' sums in order), their softmax, and k rounds of picking the largest
-// remaining logit.  Equal logits: the lower index.  A NaN orders as the lowest
-// and makes the token's weights NaN; the ids are valid whatever the logits.
-__global__ void __launch_bounds__(64) route_topk_kernel(const double* __restrict__ part, int slices, int M, int E,
-                                                        int k, int renorm, int* __restrict__ ids,
-                                                        float* __restrict__ weights) {
-  constexpr int PER = kMaxExperts / 64;
-  const int m = blockIdx.x, lane = threadIdx.x;
-  const double inf = __builtin_inf();
-  double l[PER];
-  double top = -inf;
-  bool nan = false;
+// One workgroup to a token: the logits (the slices' sums in a fixed order),
+// each expert's rank (how many logits are larger, or equal with a lower
+// number), the softmax, and the k experts of rank 0 .. k - 1.  Ranks need no
+// rounds of reductions: E comparisons in every thread.  A NaN orders as the
+// lowest and makes the token's weights NaN; the ids are valid whatever the
+// logits.
+__global__ void __launch_bounds__(256) route_topk_kernel(const double* __restrict__ part, int slices, int E, int k,
+                                                         int renorm, int* __restrict__ ids,
+                                                         float* __restrict__ weights) {
+  __shared__ double l[kMaxExperts], sums[256], top, chosen[64], wave_part[4];
+  __shared__ int nan_seen;
+  const int m = blockIdx.x, tid = threadIdx.x;
+  const double* mine = part + (int64_t)m * slices * E;
+  if (tid == 0) nan_seen = 0;
+  for (int e0 = 0; e0 < E; e0 += 256) {
+    // thread -> expert e0 + c, every rows-th slice from r on
+    const int ew = min(256, E - e0), rows = 256 / ew, r = tid / ew, c = tid - r * ew;
+    double s = 0.0;
+    if (r < rows) {
+      const double* p = mine + e0 + c;
+      int q = r;
+      for (; q + 7 * rows < slices; q += 8 * rows) {
+        double v[8];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = i * 64 + lane;
-    l[i] = -inf;
+        for (int u = 0; u < 8; ++u) v[u] = p[(int64_t)(q + u * rows) * E];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += v[u];
+      }
+      for (; q < slices; q += rows) s += p[(int64_t)q * E];
+    }
+    sums[tid] = s;
+    __syncthreads();
+    if (r == 0) {
+      for (int u = 1; u < rows; ++u) s += sums[u * ew + c];
+      if (s != s) nan_seen = 1;
+      l[e0 + c] = s != s ? -__builtin_inf() : s;
+    }
+    __syncthreads();
+  }
+  int rank[kMaxExperts / 256];
+  double total = 0.0;
+#pragma unroll
+  for (int i = 0; i < kMaxExperts / 256; ++i) {
+    const int e = i * 256 + tid;
+    rank[i] = 0;
     if (e < E) {
-      double s = 0.0;
-      for (int q = 0; q < slices; ++q) s += part[((int64_t)q * M + m) * E + e];
-      nan = nan || s != s;
-      l[i] = s != s ? -inf : s;
-      top = l[i] > top ? l[i] : top;
+      const double v = l[e];
+      int ahead = 0;
+      for (int f = 0; f < E; ++f) ahead += (l[f] > v || (l[f] == v && f < e)) ? 1 : 0;
+      rank[i] = ahead;
+      if (ahead == 0) top = v;
     }
   }
+  __syncthreads();
+  double p[kMaxExperts / 256];
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    const double o = shfl_xor_f64(top, d);
-    top = o > top ? o : top;
+  for (int i = 0; i < kMaxExperts / 256; ++i) {
+    const int e = i * 256 + tid;
+    p[i] = 0.0;
+    if (e < E) p[i] = exp(l[e] - top);
+    total += p[i];
   }
-  nan = __ballot(nan) != 0ull;
-  double sum = 0.0;
 #pragma unroll
-  for (int i = 0; i < PER; ++i)
-    if (i * 64 + lane < E) sum += exp(l[i] - top);
+  for (int d = 32; d >= 1; d >>= 1) total += shfl_xor_f64(total, d);
+  if ((tid & 63) == 0) wave_part[tid >> 6] = total;
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) sum += shfl_xor_f64(sum, d);
-  uint32_t taken = 0;
-  double kept = 0.0, mine = 0.0;
-  for (int j = 0; j < k; ++j) {
-    double best = -inf;
-    int at = 1 << 30;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = i * 64 + lane;
-      if (e < E && !((taken >> i) & 1u) && (at == 1 << 30 || l[i] > best)) {
-        best = l[i];
-        at = e;
-      }
-    }
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-      const double ob = shfl_xor_f64(best, d);
-      const int oa = __shfl_xor(at, d, 64);
-      if (ob > best || (ob == best && oa < at)) {
-        best = ob;
-        at = oa;
-      }
-    }
-    if ((at & 63) == lane) taken |= 1u << (at >> 6);
-    const double p = exp(best - top) / sum;
-    kept += p;
-    if (lane == j) {
-      mine = p;
-      ids[(int64_t)m * k + j] = at;
+  for (int i = 0; i < kMaxExperts / 256; ++i) {
+    const int e = i * 256 + tid;
+    if (e < E && rank[i] < k) {
+      chosen[rank[i]] = p[i];
+      ids[(int64_t)m * k + rank[i]] = e;
     }
   }
-  if (lane < k) {
-    double w = renorm ? mine / kept : mine;
-    if (nan) w = __builtin_nan("");
-    weights[(int64_t)m * k + lane] = (float)w;
+  __syncthreads();
+  if (tid < k) {
+    double sum = 0.0;
+    if (renorm)
+      for (int u = 0; u < k; ++u) sum += chosen[u];
+    else
+      sum = (wave_part[0] + wave_part[1]) + (wave_part[2] + wave_part[3]);
+    weights[(int64_t)m * k + tid] = nan_seen ? __builtin_nanf("") : (float)(chosen[tid] / sum);
   }
 }
 
@@ -170,17 +173,37 @@ struct FewArgs {
   int splits;           // parts of K, blockIdx.z
 };
 
+// The rows of one expert.  Up to 64 pairs: a wave holds them in a register
+// (lane i: the i-th row) and every wave finds them for itself.  More: in LDS.
 struct Rows {
   uint32_t seen[kMaxExperts / 32];
   uint16_t row[kMaxPairs];
 };
 
-// The slot-th expert, in order of its number, that any id names, and its rows
-// in order.  False when there is no such expert (for the whole workgroup).  Ids
-// outside [0, E) name none.  Two barriers and a third after the rows.
-template <int THREADS>
-__device__ __forceinline__ bool find_expert(const FewArgs& a, int slot, Rows& sh, int& expert, int& n) {
+// The slot-th expert that the ids name and its rows in order, false when there
+// is none (for the whole workgroup).  Ids outside [0, E) name none.  Up to 64
+// pairs the experts come in the order of their first pair, and nothing needs a
+// barrier; else in that of their number.
+template <int THREADS, bool FEW>
+__device__ __forceinline__ bool find_expert(const FewArgs& a, int slot, Rows& sh, int& expert, int& n, int& rows) {
   const int tid = threadIdx.x, lane = tid & 63;
+  if constexpr (FEW) {
+    const int id = lane < a.P ? a.ids[lane] : -1;
+    unsigned long long left = __ballot((unsigned)id < (unsigned)a.E), same = 0;
+    for (int s = 0; s <= slot; ++s) {
+      if (left == 0ull) return false;
+      expert = __builtin_amdgcn_readlane(id, __ffsll((long long)left) - 1);
+      same = __ballot(id == expert);
+      left &= ~same;
+    }
+    n = __popcll(same);
+    // lane i <- the lane of the i-th row: every lane sends its number to its
+    // rank among the rows, or behind them
+    const unsigned long long below = (1ull << lane) - 1ull;
+    const int rank = (same >> lane) & 1ull ? __popcll(same & below) : n + __popcll(~same & below);
+    rows = __builtin_amdgcn_ds_permute(rank * 4, lane);
+    return true;
+  }
   if (tid < kMaxExperts / 32) sh.seen[tid] = 0;
   __syncthreads();
   for (int p = tid; p < a.P; p += THREADS) {
@@ -200,8 +223,7 @@ __device__ __forceinline__ bool find_expert(const FewArgs& a, int slot, Rows& sh
   const unsigned long long hit = __ballot(here);
   if (hit == 0ull) return false;
   for (int r = slot - (incl - cnt); here && r > 0; --r) word &= word - 1u;
-  const int src = __ffsll((long long)hit) - 1;
-  expert = __builtin_amdgcn_readfirstlane(__shfl(lane * 32 + __ffs((int)word) - 1, src, 64));
+  expert = __builtin_amdgcn_readlane(lane * 32 + __ffs((int)word) - 1, __ffsll((long long)hit) - 1);
   n = 0;
   for (int p0 = 0; p0 < a.P; p0 += 64) {
     const bool mine = p0 + lane < a.P && a.ids[p0 + lane] == expert;
@@ -209,12 +231,21 @@ __device__ __forceinline__ bool find_expert(const FewArgs& a, int slot, Rows& sh
     if (tid < 64 && mine) sh.row[n + __popcll(b & ((1ull << lane) - 1ull))] = (uint16_t)(p0 + lane);
     n += __popcll(b);
   }
-  n = __builtin_amdgcn_readfirstlane(n);
   __syncthreads();
   return true;
 }
 
-__device__ __forceinline__ u32x4 stream16(const uint16_t* p) { return __builtin_nontemporal_load((const u32x4*)p); }
+// Loads of the main loop are buffer loads: a scalar descriptor, a lane offset
+// held for the whole loop and a scalar offset.  (As global loads the compiler
+// kept a 64-bit address in registers for each of a step's rows, which spilled.)
+typedef __amdgpu_buffer_rsrc_t brsrc_t;
+__device__ __forceinline__ brsrc_t range_of(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
+}
+template <bool STREAM>
+__device__ __forceinline__ u32x4 load16(brsrc_t r, uint32_t lane_at, uint32_t at) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, (int)lane_at, (int)at, STREAM ? 2 : 0);
+}
 
 // One workgroup: up to 16 * NT rows of one expert times 128 columns of its
 // matrix over one part of K.
@@ -232,14 +263,19 @@ __device__ __forceinline__ u32x4 stream16(const uint16_t* p) { return __builtin_
 // (chunks 8..15).  Without a split of K the workgroup has all of left and gate of
 // its channels and writes h itself, in two bf16 halves whose sum carries 16 bits
 // (the second product of the down matrix costs no time: HBM bounds it).
-template <int NT, int WAVES, bool GATE>
-__global__ void __launch_bounds__(WAVES * 64) few_kernel(const FewArgs a) {
+template <int NT, int WAVES, bool GATE, bool FEW>
+__global__ void __launch_bounds__(WAVES * 64, NT == 1 ? 4 : 2) few_kernel(const FewArgs a) {
   __shared__ Rows sh;
   __shared__ f32x4 sums[WAVES][8][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  int expert, n;
-  if (!find_expert<WAVES * 64>(a, blockIdx.y, sh, expert, n)) return;
+  int expert, n, rows;
+  if (!find_expert<WAVES * 64, FEW>(a, blockIdx.y, sh, expert, n, rows)) return;
+  // row i of the expert, i < n
+  auto row_of = [&](int i) -> int {
+    if constexpr (FEW) return __shfl(rows, i, 64);
+    else return sh.row[i];
+  };
   const int j = lane & 15, g = lane >> 4;
   const int I = a.N / 2;
   int col;  // of this lane's chunk
@@ -248,16 +284,19 @@ __global__ void __launch_bounds__(WAVES * 64) few_kernel(const FewArgs a) {
   const int steps = a.K / 32;
   const int s0 = steps * (int)blockIdx.z / a.splits, s1 = steps * ((int)blockIdx.z + 1) / a.splits;
   const int first = s0 + wave, cnt = first < s1 ? (s1 - first + WAVES - 1) / WAVES : 0;
-  const uint16_t* wbase = a.w + (int64_t)expert * a.K * a.N + (int64_t)(g * 8) * a.N + col;
+  const uint16_t* wbase = a.w + (int64_t)expert * a.K * a.N;
+  const uint32_t lane_at = (uint32_t)((g * 8 * a.N + col) * 2), pitch = (uint32_t)a.N * 2u;
   constexpr int PARTS = GATE ? 1 : 2;  // bf16 parts of an operand row
+  const uint32_t part_bytes = (uint32_t)(GATE ? a.P / a.k : a.P) * (uint32_t)a.K * 2u;  // at most 2^29
+  const brsrc_t xr = range_of(a.x, part_bytes * PARTS);
 
   for (int r0 = 0; r0 < n; r0 += 16 * NT) {
     const int nt = min(NT, (n - r0 + 15) / 16);
-    const uint16_t* xrow[NT];
+    uint32_t xrow[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int p = sh.row[min(r0 + t * 16 + j, n - 1)];
-      xrow[t] = a.x + (int64_t)(GATE ? p / a.k : p) * a.K + g * 8;
+      const int p = row_of(min(r0 + t * 16 + j, n - 1));
+      xrow[t] = ((uint32_t)(GATE ? p / a.k : p) * (uint32_t)a.K + (uint32_t)g * 8u) * 2u;
     }
     f32x4 acc[NT][8];
 #pragma unroll
@@ -269,14 +308,17 @@ __global__ void __launch_bounds__(WAVES * 64) few_kernel(const FewArgs a) {
       u32x4 x[NT][PARTS];
     };
     auto load = [&](int i, Step& q) {
-      const int64_t kk = (int64_t)(first + i * WAVES) * 32;
-      const uint16_t* p = wbase + kk * a.N;
-#pragma unroll
-      for (int r = 0; r < 8; ++r) q.w[r] = stream16(p + (int64_t)r * a.N);
+      const int kk = (first + i * WAVES) * 32;
+      const brsrc_t wr = range_of(wbase + (int64_t)kk * a.N, 32u * pitch);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int u = 0; u < PARTS; ++u) q.x[t][u] = *(const u32x4*)(xrow[t] + (int64_t)u * a.P * a.K + kk);
+        for (int u = 0; u < PARTS; ++u) q.x[t][u] = load16<false>(xr, xrow[t], u * part_bytes + kk * 2u);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) q.w[r] = load16<true>(wr, lane_at, r * pitch);
+      // loads stay in the order of their steps: a wait for one step's never
+      // covers the next one's
+      __builtin_amdgcn_sched_barrier(0);
     };
     auto use = [&](const Step& q) {
 #pragma unroll
@@ -304,8 +346,10 @@ __global__ void __launch_bounds__(WAVES * 64) few_kernel(const FewArgs a) {
       int i = 0;
       for (; i + 3 < cnt; i += 2) {
         use(q0);
+        __builtin_amdgcn_sched_barrier(0);
         load(i + 2, q0);
         use(q1);
+        __builtin_amdgcn_sched_barrier(0);
         load(i + 3, q1);
       }
       const int rest = cnt - i;  // 1..3
@@ -336,7 +380,7 @@ __global__ void __launch_bounds__(WAVES * 64) few_kernel(const FewArgs a) {
           v[c] = f;
         }
         const bool live = r < n;
-        const int p = sh.row[live ? r : 0];
+        const int p = row_of(live ? r : 0);
         if (GATE && a.splits == 1) {
           // chunk q < 8 is left, chunk q + 8, eight lanes on, its gate
           uint16_t hi[8], lo[8];
@@ -436,11 +480,11 @@ namespace {
 using namespace swb;
 
 constexpr int64_t kFewTokens = 64;
-constexpr int64_t kFewDim = (int64_t)1 << 20;
+constexpr int64_t kFewDim = (int64_t)1 << 18;  // 1024 rows of h within 2^31 bytes
 constexpr int kUnits = 256;  // compute units of an MI355X
 constexpr int kWaves = 8;
 
-int64_t route_slices(int64_t D) { return (D + kRouteSlice - 1) / kRouteSlice; }
+int64_t route_slices(int64_t D) { return D / kRouteSlice; }
 
 // Parts of K: so many that the launch has a workgroup for every compute unit
 // when every slot has its expert, but at least a step of 32 for every wave.
@@ -496,23 +540,26 @@ size_t route_bytes(int64_t M, int64_t D, int64_t E) { return align256((size_t)(r
 int run_route(const void* x, const void* wr, int* ids, float* weights, void* ws, int64_t M, int64_t D, int64_t E,
               int64_t k, int renorm, hipStream_t st) {
   const int slices = (int)route_slices(D);
-  hipLaunchKernelGGL(route_logits_kernel,
-                     dim3((unsigned)slices, (unsigned)((M + kRouteTokens - 1) / kRouteTokens), (unsigned)((E + 255) / 256)),
-                     dim3(256), 0, st, (const uint16_t*)x, (const uint16_t*)wr, (double*)ws, (int)M, (int)D, (int)E);
+  hipLaunchKernelGGL(route_logits_kernel, dim3((unsigned)slices, (unsigned)((M + 15) / 16), (unsigned)((E + 15) / 16)),
+                     dim3(64), 0, st, (const uint16_t*)x, (const uint16_t*)wr, (double*)ws, (int)M, (int)D, (int)E);
   SW_TRY(launch_status());
-  hipLaunchKernelGGL(route_topk_kernel, dim3((unsigned)M), dim3(64), 0, st, (const double*)ws, slices, (int)M, (int)E,
-                     (int)k, renorm, ids, weights);
+  hipLaunchKernelGGL(route_topk_kernel, dim3((unsigned)M), dim3(256), 0, st, (const double*)ws, slices, (int)E, (int)k,
+                     renorm, ids, weights);
   return launch_status();
 }
 
+template <int NT, bool GATE>
+int run_few(const FewArgs& a, int64_t slots, hipStream_t st) {
+  const dim3 grid(GATE ? (unsigned)(a.N / 128) : (unsigned)((a.N + 127) / 128), (unsigned)slots, (unsigned)a.splits);
+  if (a.P <= 64) hipLaunchKernelGGL((few_kernel<NT, kWaves, GATE, true>), grid, dim3(kWaves * 64), 0, st, a);
+  else hipLaunchKernelGGL((few_kernel<NT, kWaves, GATE, false>), grid, dim3(kWaves * 64), 0, st, a);
+  return launch_status();
+}
 template <bool GATE>
 int run_few(const FewArgs& a, int64_t M, int64_t slots, hipStream_t st) {
-  const unsigned blocks = GATE ? (unsigned)(a.N / 128) : (unsigned)((a.N + 127) / 128);
-  const dim3 grid(blocks, (unsigned)slots, (unsigned)a.splits);
-  if (M <= 16) hipLaunchKernelGGL((few_kernel<1, kWaves, GATE>), grid, dim3(kWaves * 64), 0, st, a);
-  else if (M <= 32) hipLaunchKernelGGL((few_kernel<2, kWaves, GATE>), grid, dim3(kWaves * 64), 0, st, a);
-  else hipLaunchKernelGGL((few_kernel<4, kWaves, GATE>), grid, dim3(kWaves * 64), 0, st, a);
-  return launch_status();
+  if (M <= 16) return run_few<1, GATE>(a, slots, st);
+  if (M <= 32) return run_few<2, GATE>(a, slots, st);
+  return run_few<4, GATE>(a, slots, st);
 }
 
 int run_experts(const void* x, const void* W1, const void* W_down, const int* ids, const float* weights, void* y,

@@ -89,7 +89,7 @@ int swiglu_clip_grad_norm(const void* const* grads, void* const* outs, const int
  * expert MLPs of swiglu_moe_fwd without packed rows.  bf16 tensors, row-major
  * and densely packed; 0 <= M <= 64 tokens, 1 <= E <= 1024 experts,
  * 1 <= k <= 64 choices of a token (k <= E where the router makes them),
- * M * k <= 1024; D, I and Dout are positive multiples of 64 up to 2^20.  x, W1,
+ * M * k <= 1024; D, I and Dout are positive multiples of 64 up to 2^18.  x, W1,
  * W_down and y are 16-byte aligned.
  *   W_router [D,E], W1 [E,D,2I] ([left | gate]), W_down [E,I,Dout]
  *   ids int32 [M,k], weights float [M,k]

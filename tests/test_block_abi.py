@@ -142,7 +142,7 @@ def test_moe_route_refuses():
         return L.swiglu_moe_route(*q, wsb, M, D, E, k, 1, None)
     assert f(M=-1) == SHAPE and f(E=0) == SHAPE and f(k=0) == SHAPE and f(k=9) == SHAPE and f(D=0) == SHAPE
     assert f(M=65) == UNSUP and f(E=1025) == UNSUP and f(E=100, k=65) == UNSUP and f(M=64, E=64, k=17) == UNSUP
-    assert f(D=100) == UNSUP and f(D=1 << 21) == UNSUP
+    assert f(D=100) == UNSUP and f(D=1 << 19) == UNSUP
     for i in range(4):
         assert f({i: None}) == NULL, i
     assert f({0: addr(0) + 1}) == ALIGN and f({2: addr(2) + 2}) == ALIGN and f({4: addr(4) + 8}) == ALIGN
@@ -170,7 +170,7 @@ def test_moe_few_refuses():
     for f, last in ((few, 6), (layer, 7)):
         assert f(M=-1) == SHAPE and f(E=0) == SHAPE and f(k=0) == SHAPE and f(I=0) == SHAPE and f(Dout=-64) == SHAPE
         assert f(E=100, k=65) == UNSUP and f(M=64, E=20, k=17) == UNSUP
-        assert f(M=65) == UNSUP and f(I=96) == UNSUP and f(Dout=100) == UNSUP and f(D=(1 << 20) + 64) == UNSUP
+        assert f(M=65) == UNSUP and f(I=96) == UNSUP and f(Dout=100) == UNSUP and f(D=(1 << 18) + 64) == UNSUP
         for i in range(last):
             assert f({i: None}) == NULL, i
         assert f({0: addr(0) + 2}) == ALIGN and f({last: addr(last) + 8}) == ALIGN
