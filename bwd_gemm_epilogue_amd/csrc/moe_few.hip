@@ -7,14 +7,20 @@
 //   e = ids[m,j]
 //
 // With at most 64 tokens every weight is used for a few multiply-adds only, so
-// the layer is a stream of the chosen experts' weights from HBM.  A pair (token
-// m, choice j) is a row m*k + j.  Four kinds of launch:
+// the layer is a stream of the chosen experts' weights from HBM; what costs
+// beside it are launches, so there are few.  A pair (token m, choice j) is a row
+// m*k + j.
 //   * logits: partial sums of x Wr over slices of D, in 64 bits, so that the
 //     choice does not depend on the order of the sum;
-//   * top-k: one wave to a token;
-//   * gate/up and down: a workgroup finds its expert among the ids, gathers the
-//     expert's rows, and streams one block of 128 columns of its matrix;
-//   * combine: the weighted sum of the rows' results, in a fixed order.
+//   * top-k: a workgroup to a token; for a token or a few, every workgroup of
+//     the next launch does it for itself instead;
+//   * gate/up: a workgroup finds its expert among the ids, gathers the expert's
+//     rows, and streams one block of 128 columns of W1 (64 of left, 64 of gate);
+//   * down: the same on W_down, 128 columns; where K of the gate/up was split,
+//     it first makes h of its rows from the parts;
+//   * combine: the weighted sum of the rows' results, in a fixed order.  (By the
+//     last workgroup of a block of columns to arrive it took as long for a token
+//     and longer for more: 134 -> 149 us at 32, 166 with device-scope fences.)
 #include "block_common.hpp"
 #include "swiglu_math.hpp"
 
@@ -30,37 +36,44 @@ constexpr int kMaxPairs = 1024, kMaxExperts = 1024;
 // Router
 // ---------------------------------------------------------------------------
 typedef double f64x4 __attribute__((ext_vector_type(4)));
-constexpr int kRouteSlice = 64;  // rows of Wr of one wave; D is a multiple
-
-__device__ __forceinline__ double bf16_f64(uint32_t bits) { return (double)swg::bf16_lo(bits); }
+constexpr int kRouteWaves = 4;
+constexpr int kRouteSlice = kRouteWaves * 64;  // rows of Wr of one workgroup, 64 of each wave
 
 // part[m][slice][e] = sum over the slice's d of x[m,d] Wr[d,e] in 64 bits: a
 // product of two bf16 values is exact there, and the sum is off by 2^-53 a term.
-// One wave: 16 tokens, 16 experts, 64 d, sixteen v_mfma_f64_16x16x4.  Lane 16 g +
-// j holds token j's and expert j's values at d = 8 g + i (and 32 + 8 g + i) in
-// step i, so a token's eight are one load.
-__global__ void __launch_bounds__(64) route_logits_kernel(const uint16_t* __restrict__ x,
-                                                          const uint16_t* __restrict__ wr, double* __restrict__ part,
-                                                          int M, int D, int E) {
-  const int lane = threadIdx.x, j = lane & 15, g = lane >> 4;
-  const int d0 = blockIdx.x * kRouteSlice, m0 = blockIdx.y * 16, e0 = blockIdx.z * 16;
-  const uint16_t* xp = x + (int64_t)min(m0 + j, M - 1) * D + d0 + g * 8;
-  const uint16_t* wp = wr + (int64_t)(d0 + g * 8) * E + min(e0 + j, E - 1);
-  uint16_t xv[2][8], wv[2][8];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      xv[h][i] = xp[h * 32 + i];
-      wv[h][i] = wp[(int64_t)(h * 32 + i) * E];
-    }
-  }
+// One workgroup: 16 tokens, 16 experts, 256 d; a wave has 64 of them, in sixteen
+// v_mfma_f64_16x16x4.  Lane 16 g + j holds token j's and expert j's values at d =
+// 8 g + i (and 32 + 8 g + i) in step i, so a token's eight are one load.
+__global__ void __launch_bounds__(kRouteWaves * 64) route_logits_kernel(const uint16_t* __restrict__ x,
+                                                           const uint16_t* __restrict__ wr, double* __restrict__ part,
+                                                           int M, int D, int E) {
+  __shared__ f64x4 sums[kRouteWaves - 1][64];
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int d0 = blockIdx.x * kRouteSlice + wave * 64, m0 = blockIdx.y * 16, e0 = blockIdx.z * 16;
   f64x4 acc = {};
+  if (d0 < D) {  // D is a multiple of 64: a wave's rows are all there or none
+    const uint16_t* xp = x + (int64_t)min(m0 + j, M - 1) * D + d0 + g * 8;
+    const uint16_t* wp = wr + (int64_t)(d0 + g * 8) * E + min(e0 + j, E - 1);
+    Vec<bf16_t>::type xv[2];
+    uint16_t wv[2][8];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      xv[h] = load_vec((const bf16_t*)xp + h * 32);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      acc = __builtin_amdgcn_mfma_f64_16x16x4f64(bf16_f64(xv[h][i]), bf16_f64(wv[h][i]), acc, 0, 0, 0);
+      for (int i = 0; i < 8; ++i) wv[h][i] = wp[(int64_t)(h * 32 + i) * E];
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)(float)xv[h][i], (double)swg::bf16_lo(wv[h][i]), acc, 0, 0, 0);
+  }
+  if (wave > 0) sums[wave - 1][lane] = acc;
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int w = 0; w < kRouteWaves - 1; ++w) acc += sums[w][lane];
   // acc[r]: token 4 r + g, expert j
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
@@ -69,114 +82,104 @@ __global__ void __launch_bounds__(64) route_logits_kernel(const uint16_t* __rest
   }
 }
 
-__device__ __forceinline__ double shfl_xor_f64(double v, int d) {
-  int2 b = __builtin_bit_cast(int2, v);
-  b.x = __shfl_xor(b.x, d, 64);
-  b.y = __shfl_xor(b.y, d, 64);
-  return __builtin_bit_cast(double, b);
+// A logit: its slices' sums in order.  Sixteen loads at a time, past the end the
+// last slice again: a load for each turn of a loop would wait for each.
+__device__ __forceinline__ double logit_of(const double* part, int slices, int E) {
+  double s = 0.0;
+  for (int q = 0; q < slices; q += 16) {
+    double v[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) v[u] = part[(int64_t)min(q + u, slices - 1) * E];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) s += q + u < slices ? v[u] : 0.0;
+  }
+  return s;
 }
 
-// One workgroup to a token: the logits (the slices' sums in a fixed order),
-// each expert's rank (how many logits are larger, or equal with a lower
-// number), the softmax, and the k experts of rank 0 .. k - 1.  Ranks need no
-// rounds of reductions: E comparisons in every thread.  A NaN orders as the
-// lowest and makes the token's weights NaN; the ids are valid whatever the
+// An expert's rank among a token's logits: how many are larger, or equal with a
+// lower number.  A NaN has been put in as -inf: the lowest.
+__device__ __forceinline__ int rank_of(const double* l, int E, int e) {
+  const double v = l[e];
+  int ahead = 0;
+  for (int f = 0; f < E; ++f) ahead += (l[f] > v || (l[f] == v && f < e)) ? 1 : 0;
+  return ahead;
+}
+
+__device__ __forceinline__ double wave_sum_f64(double v) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+
+// One wave: the weights of a token's chosen experts (first: that of the largest
+// logit) from its E logits.
+__device__ __forceinline__ void route_weights(const double* l, const int* chosen, int E, int k, int renorm, bool nan,
+                                              float* weights) {
+  const int lane = threadIdx.x & 63;
+  const double top = l[chosen[0]];
+  const double p = lane < k ? exp(l[chosen[lane]] - top) : 0.0;
+  double sum = p;
+  if (!renorm) {
+    sum = 0.0;
+    for (int e = lane; e < E; e += 64) sum += exp(l[e] - top);
+  }
+  sum = wave_sum_f64(sum);
+  if (lane < k) weights[lane] = nan ? __builtin_nanf("") : (float)(p / sum);
+}
+
+// One workgroup to a token: logits, ranks, and the k experts of rank 0 .. k - 1.
+// A NaN logit makes the token's weights NaN; the ids are valid whatever the
 // logits.
 __global__ void __launch_bounds__(256) route_topk_kernel(const double* __restrict__ part, int slices, int E, int k,
                                                          int renorm, int* __restrict__ ids,
                                                          float* __restrict__ weights) {
-  __shared__ double l[kMaxExperts], sums[256], top, chosen[64], wave_part[4];
-  __shared__ int nan_seen;
+  __shared__ double l[kMaxExperts];
+  __shared__ int chosen[64], nan_seen;
   const int m = blockIdx.x, tid = threadIdx.x;
-  const double* mine = part + (int64_t)m * slices * E;
   if (tid == 0) nan_seen = 0;
-  for (int e0 = 0; e0 < E; e0 += 256) {
-    // thread -> expert e0 + c, every rows-th slice from r on
-    const int ew = min(256, E - e0), rows = 256 / ew, r = tid / ew, c = tid - r * ew;
-    double s = 0.0;
-    if (r < rows) {
-      const double* p = mine + e0 + c;
-      int q = r;
-      for (; q + 7 * rows < slices; q += 8 * rows) {
-        double v[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = p[(int64_t)(q + u * rows) * E];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) s += v[u];
-      }
-      for (; q < slices; q += rows) s += p[(int64_t)q * E];
-    }
-    sums[tid] = s;
-    __syncthreads();
-    if (r == 0) {
-      for (int u = 1; u < rows; ++u) s += sums[u * ew + c];
-      if (s != s) nan_seen = 1;
-      l[e0 + c] = s != s ? -__builtin_inf() : s;
-    }
-    __syncthreads();
+  __syncthreads();
+  for (int e = tid; e < E; e += 256) {
+    const double s = logit_of(part + (int64_t)m * slices * E + e, slices, E);
+    if (s != s) nan_seen = 1;
+    l[e] = s != s ? -__builtin_inf() : s;
   }
-  int rank[kMaxExperts / 256];
-  double total = 0.0;
-#pragma unroll
-  for (int i = 0; i < kMaxExperts / 256; ++i) {
-    const int e = i * 256 + tid;
-    rank[i] = 0;
-    if (e < E) {
-      const double v = l[e];
-      int ahead = 0;
-      for (int f = 0; f < E; ++f) ahead += (l[f] > v || (l[f] == v && f < e)) ? 1 : 0;
-      rank[i] = ahead;
-      if (ahead == 0) top = v;
+  __syncthreads();
+  for (int e = tid; e < E; e += 256) {
+    const int r = rank_of(l, E, e);
+    if (r < k) {
+      chosen[r] = e;
+      ids[(int64_t)m * k + r] = e;
     }
   }
   __syncthreads();
-  double p[kMaxExperts / 256];
-#pragma unroll
-  for (int i = 0; i < kMaxExperts / 256; ++i) {
-    const int e = i * 256 + tid;
-    p[i] = 0.0;
-    if (e < E) p[i] = exp(l[e] - top);
-    total += p[i];
-  }
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) total += shfl_xor_f64(total, d);
-  if ((tid & 63) == 0) wave_part[tid >> 6] = total;
-#pragma unroll
-  for (int i = 0; i < kMaxExperts / 256; ++i) {
-    const int e = i * 256 + tid;
-    if (e < E && rank[i] < k) {
-      chosen[rank[i]] = p[i];
-      ids[(int64_t)m * k + rank[i]] = e;
-    }
-  }
-  __syncthreads();
-  if (tid < k) {
-    double sum = 0.0;
-    if (renorm)
-      for (int u = 0; u < k; ++u) sum += chosen[u];
-    else
-      sum = (wave_part[0] + wave_part[1]) + (wave_part[2] + wave_part[3]);
-    weights[(int64_t)m * k + tid] = nan_seen ? __builtin_nanf("") : (float)(chosen[tid] / sum);
-  }
+  if (tid < 64) route_weights(l, chosen, E, k, renorm, nan_seen != 0, weights + (int64_t)m * k);
 }
 
 // ---------------------------------------------------------------------------
 // The experts' matrices
 // ---------------------------------------------------------------------------
 struct FewArgs {
-  const uint16_t* x;    // gate/up: [M, K] bf16.  down: h, its upper half of bits [P, K] and then its lower half
-  const uint16_t* w;    // [E, K, N] bf16
-  const int* ids;       // [P]
-  float* part;          // [splits][P][N] partial sums
-  uint16_t* h;          // gate/up without split: [2][P][N / 2]
+  const uint16_t* x;      // gate/up: [M, K] bf16.  down: h, its upper half of bits [P, K] and then its lower half
+  const uint16_t* w;      // [E, K, N] bf16
+  int* ids;               // [P]; written by the gate/up launch where it routes
+  float* part;            // [splits][P][N] partial sums
+  uint16_t* h;            // gate/up without split: [2][P][N / 2]
   int P, E, k, K, N;
-  int splits;           // parts of K, blockIdx.z
+  int splits;             // parts of K, blockIdx.z
+  // gate/up that routes: the logits' slices
+  const double* logits;
+  int slices, renorm;
+  float* weights;         // [P]
+  // down from the gate/up's parts: [gate_splits][P][2 K]
+  const float* gate_part;
+  int gate_splits;
 };
 
 // The rows of one expert.  Up to 64 pairs: a wave holds them in a register
 // (lane i: the i-th row) and every wave finds them for itself.  More: in LDS.
 struct Rows {
   uint32_t seen[kMaxExperts / 32];
+  int16_t id[kMaxPairs];  // -1: none
   uint16_t row[kMaxPairs];
 };
 
@@ -185,10 +188,11 @@ struct Rows {
 // pairs the experts come in the order of their first pair, and nothing needs a
 // barrier; else in that of their number.
 template <int THREADS, bool FEW>
-__device__ __forceinline__ bool find_expert(const FewArgs& a, int slot, Rows& sh, int& expert, int& n, int& rows) {
+__device__ __forceinline__ bool find_expert(const FewArgs& a, const int* ids, int slot, Rows& sh, int& expert, int& n,
+                                            int& rows) {
   const int tid = threadIdx.x, lane = tid & 63;
   if constexpr (FEW) {
-    const int id = lane < a.P ? a.ids[lane] : -1;
+    const int id = lane < a.P ? ids[lane] : -1;
     unsigned long long left = __ballot((unsigned)id < (unsigned)a.E), same = 0;
     for (int s = 0; s <= slot; ++s) {
       if (left == 0ull) return false;
@@ -207,8 +211,10 @@ __device__ __forceinline__ bool find_expert(const FewArgs& a, int slot, Rows& sh
   if (tid < kMaxExperts / 32) sh.seen[tid] = 0;
   __syncthreads();
   for (int p = tid; p < a.P; p += THREADS) {
-    const int id = a.ids[p];
-    if ((unsigned)id < (unsigned)a.E) atomicOr(&sh.seen[id >> 5], 1u << (id & 31));
+    const int id = ids[p];
+    const bool valid = (unsigned)id < (unsigned)a.E;
+    sh.id[p] = (int16_t)(valid ? id : -1);
+    if (valid) atomicOr(&sh.seen[id >> 5], 1u << (id & 31));
   }
   __syncthreads();
   uint32_t word = lane < kMaxExperts / 32 ? sh.seen[lane] : 0u;
@@ -226,7 +232,7 @@ __device__ __forceinline__ bool find_expert(const FewArgs& a, int slot, Rows& sh
   expert = __builtin_amdgcn_readlane(lane * 32 + __ffs((int)word) - 1, __ffsll((long long)hit) - 1);
   n = 0;
   for (int p0 = 0; p0 < a.P; p0 += 64) {
-    const bool mine = p0 + lane < a.P && a.ids[p0 + lane] == expert;
+    const bool mine = p0 + lane < a.P && sh.id[p0 + lane] == expert;
     const unsigned long long b = __ballot(mine);
     if (tid < 64 && mine) sh.row[n + __popcll(b & ((1ull << lane) - 1ull))] = (uint16_t)(p0 + lane);
     n += __popcll(b);
@@ -259,18 +265,66 @@ __device__ __forceinline__ u32x4 load16(brsrc_t r, uint32_t lane_at, uint32_t at
 // No LDS, no barrier, and two steps of loads in flight in each wave; the waves
 // take every WAVES-th step and their sums meet in LDS at the end.
 //
-// GATE: W1, columns 64 b .. + 63 of the left half beside those of the gate half
+// Gate/up: W1, columns 64 b .. + 63 of the left half beside those of the gate half
 // (chunks 8..15).  Without a split of K the workgroup has all of left and gate of
 // its channels and writes h itself, in two bf16 halves whose sum carries 16 bits
 // (the second product of the down matrix costs no time: HBM bounds it).
-template <int NT, int WAVES, bool GATE, bool FEW>
-__global__ void __launch_bounds__(WAVES * 64, NT == 1 ? 4 : 2) few_kernel(const FewArgs a) {
+// Four waves: with eight 32 tokens take 134 us instead of 132, 64 tokens over 64
+// experts 129 instead of 108 (fewer workgroups on a compute unit, whose starts
+// and ends the others' loads have to hide).
+template <int V>
+struct int_c {
+  static constexpr int value = V;
+};
+
+enum Kind {
+  kGate,       // ids are given
+  kGateRoute,  // ids from the logits, up to kRouteInline of them; P <= 64
+  kDown,       // from h
+  kDownPart    // from the gate/up's parts
+};
+constexpr int kRouteInline = 256;  // logits (tokens times experts)
+constexpr int kPartRows = 16, kPartValues = 8192;  // rows and values of h that a kDownPart workgroup makes
+
+template <int NT, int WAVES, Kind KIND, bool FEW, int AHEAD>
+__global__ void __launch_bounds__(WAVES * 64, AHEAD > 2 ? 1 : NT == 1 ? 4 : 2) few_kernel(const FewArgs a) {
+  constexpr bool GATE = KIND == kGate || KIND == kGateRoute;
+  constexpr int THREADS = WAVES * 64;
   __shared__ Rows sh;
   __shared__ f32x4 sums[WAVES][8][64];
+  __shared__ __attribute__((aligned(16))) uint16_t hs[KIND == kDownPart ? 2 * (kPartValues + kPartRows * 8) : 1];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  int expert, n, rows;
-  if (!find_expert<WAVES * 64, FEW>(a, blockIdx.y, sh, expert, n, rows)) return;
+  const int* ids = a.ids;
+  if constexpr (KIND == kGateRoute) {
+    // every workgroup ranks the logits for itself; the first one writes the result
+    __shared__ double l[kRouteInline];
+    __shared__ int chosen[64], nan_seen[64];
+    const int M = a.P / a.k;
+    if (tid < 64) nan_seen[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < M * a.E; i += THREADS) {
+      const int m = i / a.E;
+      const double s = logit_of(a.logits + (int64_t)m * a.slices * a.E + (i - m * a.E), a.slices, a.E);
+      if (s != s) nan_seen[m] = 1;
+      l[i] = s != s ? -__builtin_inf() : s;
+    }
+    __syncthreads();
+    for (int i = tid; i < M * a.E; i += THREADS) {
+      const int m = i / a.E, e = i - m * a.E;
+      const int r = rank_of(l + m * a.E, a.E, e);
+      if (r < a.k) chosen[m * a.k + r] = e;
+    }
+    __syncthreads();
+    ids = chosen;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
+      if (tid < a.P) a.ids[tid] = chosen[tid];
+      for (int t = wave; t < M; t += WAVES)
+        route_weights(l + t * a.E, chosen + t * a.k, a.E, a.k, a.renorm, nan_seen[t] != 0, a.weights + t * a.k);
+    }
+  }
+  int expert, n, rows = 0;
+  if (!find_expert<THREADS, FEW>(a, ids, blockIdx.y, sh, expert, n, rows)) return;
   // row i of the expert, i < n
   auto row_of = [&](int i) -> int {
     if constexpr (FEW) return __shfl(rows, i, 64);
@@ -280,7 +334,7 @@ __global__ void __launch_bounds__(WAVES * 64, NT == 1 ? 4 : 2) few_kernel(const 
   const int I = a.N / 2;
   int col;  // of this lane's chunk
   if constexpr (GATE) col = blockIdx.x * 64 + (j & 7) * 8 + (j >> 3) * I;
-  else col = min(blockIdx.x * 128 + j * 8, a.N - 8);
+  else col = min((int)blockIdx.x * 128 + j * 8, a.N - 8);
   const int steps = a.K / 32;
   const int s0 = steps * (int)blockIdx.z / a.splits, s1 = steps * ((int)blockIdx.z + 1) / a.splits;
   const int first = s0 + wave, cnt = first < s1 ? (s1 - first + WAVES - 1) / WAVES : 0;
@@ -289,31 +343,73 @@ __global__ void __launch_bounds__(WAVES * 64, NT == 1 ? 4 : 2) few_kernel(const 
   constexpr int PARTS = GATE ? 1 : 2;  // bf16 parts of an operand row
   const uint32_t part_bytes = (uint32_t)(GATE ? a.P / a.k : a.P) * (uint32_t)a.K * 2u;  // at most 2^29
   const brsrc_t xr = range_of(a.x, part_bytes * PARTS);
-
-  for (int r0 = 0; r0 < n; r0 += 16 * NT) {
-    const int nt = min(NT, (n - r0 + 15) / 16);
-    uint32_t xrow[NT];
+  const int width = (s1 - s0) * 32, hpitch = width + 8;  // of h in LDS (16 bytes apart in the banks)
+  if constexpr (KIND == kDownPart) {
+    // h of the expert's rows (at most 16) over this workgroup's k, four values to
+    // a thread; past the end the last ones again, since row_of reads other lanes
+    const int total = n * (width / 4);
+    for (int q0 = 0; q0 < total; q0 += THREADS) {
+      const int q = min(q0 + tid, total - 1);
+      const int r = q / (width / 4), c = (q - r * (width / 4)) * 4;
+      const float* p = a.gate_part + (int64_t)row_of(r) * 2 * a.K + s0 * 32 + c;
+      f32x4 left = {}, gate = {};
+      for (int u = 0; u < a.gate_splits; ++u) {
+        left += *(const f32x4*)(p + (int64_t)u * a.P * 2 * a.K);
+        gate += *(const f32x4*)(p + (int64_t)u * a.P * 2 * a.K + a.K);
+      }
+      uint16_t hi[4], lo[4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int p = row_of(min(r0 + t * 16 + j, n - 1));
-      xrow[t] = ((uint32_t)(GATE ? p / a.k : p) * (uint32_t)a.K + (uint32_t)g * 8u) * 2u;
+      for (int v = 0; v < 4; ++v) {
+        const float hv = swg::swiglu_h(left[v], gate[v]);
+        const bf16_t t = (bf16_t)hv;
+        hi[v] = __builtin_bit_cast(uint16_t, t);
+        lo[v] = __builtin_bit_cast(uint16_t, (bf16_t)(hv - (float)t));
+      }
+      uint16_t* o = hs + r * hpitch + c;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        o[v] = hi[v];
+        o[n * hpitch + v] = lo[v];
+      }
     }
-    f32x4 acc[NT][8];
+    __syncthreads();
+  }
+
+  // 16 T rows from r0 on
+  auto pass = [&](auto tiles, int r0) {
+    constexpr int T = decltype(tiles)::value;
+    constexpr int A = T == 4 ? 1 : AHEAD;  // four tiles' sums leave registers for one step
+    const int nt = min(T, (n - r0 + 15) / 16);
+    uint32_t xrow[T];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < T; ++t) {
+      const int i = min(r0 + t * 16 + j, n - 1);
+      if constexpr (KIND == kDownPart) {
+        xrow[t] = (uint32_t)(i * hpitch + g * 8);
+      } else {
+        const int p = row_of(i);
+        xrow[t] = ((uint32_t)(GATE ? p / a.k : p) * (uint32_t)a.K + (uint32_t)g * 8u) * 2u;
+      }
+    }
+    f32x4 acc[T][8];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
 #pragma unroll
       for (int c = 0; c < 8; ++c) acc[t][c] = f32x4{};
     struct Step {
       u32x4 w[8];
-      u32x4 x[NT][PARTS];
+      u32x4 x[T][PARTS];
     };
     auto load = [&](int i, Step& q) {
       const int kk = (first + i * WAVES) * 32;
       const brsrc_t wr = range_of(wbase + (int64_t)kk * a.N, 32u * pitch);
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < T; ++t)
 #pragma unroll
-        for (int u = 0; u < PARTS; ++u) q.x[t][u] = load16<false>(xr, xrow[t], u * part_bytes + kk * 2u);
+        for (int u = 0; u < PARTS; ++u) {
+          if constexpr (KIND == kDownPart) q.x[t][u] = *(const u32x4*)(hs + xrow[t] + u * n * hpitch + (kk - s0 * 32));
+          else q.x[t][u] = load16<false>(xr, xrow[t], u * part_bytes + kk * 2u);
+        }
 #pragma unroll
       for (int r = 0; r < 8; ++r) q.w[r] = load16<true>(wr, lane_at, r * pitch);
       // loads stay in the order of their steps: a wait for one step's never
@@ -329,45 +425,46 @@ __global__ void __launch_bounds__(WAVES * 64, NT == 1 ? 4 : 2) few_kernel(const 
           b[r] = __builtin_amdgcn_perm(q.w[2 * r + 1][c >> 1], q.w[2 * r][c >> 1], (c & 1) ? 0x07060302u : 0x05040100u);
         const bf16x8 wb = __builtin_bit_cast(bf16x8, b);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (t == 0 || t < nt) {
+        for (int t = 0; t < T; ++t)
 #pragma unroll
-            for (int u = 0; u < PARTS; ++u)
-              acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, q.x[t][u]), wb, acc[t][c],
-                                                                  0, 0, 0);
-          }
-        }
+          for (int u = 0; u < PARTS; ++u)
+            acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, q.x[t][u]), wb, acc[t][c], 0,
+                                                                0, 0);
       }
+      __builtin_amdgcn_sched_barrier(0);
     };
     if (cnt > 0) {
-      Step q0, q1;
-      load(0, q0);
-      load(cnt > 1 ? 1 : 0, q1);
+      Step q[A];
+#pragma unroll
+      for (int u = 0; u < A; ++u) load(min(u, cnt - 1), q[u]);
       int i = 0;
-      for (; i + 3 < cnt; i += 2) {
-        use(q0);
-        __builtin_amdgcn_sched_barrier(0);
-        load(i + 2, q0);
-        use(q1);
-        __builtin_amdgcn_sched_barrier(0);
-        load(i + 3, q1);
+      for (; i + 2 * A <= cnt; i += A) {
+#pragma unroll
+        for (int u = 0; u < A; ++u) {
+          use(q[u]);
+          load(i + A + u, q[u]);
+        }
       }
-      const int rest = cnt - i;  // 1..3
-      use(q0);
-      if (rest == 3) load(i + 2, q0);
-      if (rest >= 2) use(q1);
-      if (rest == 3) use(q0);
+      // the last A .. 2 A - 1 steps (fewer where there are fewer in all)
+#pragma unroll
+      for (int u = 0; u < A; ++u) {
+        if (i + u < cnt) use(q[u]);
+        if (i + A + u < cnt) load(i + A + u, q[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < A; ++u)
+        if (i + A + u < cnt) use(q[u]);
     }
     // acc[t][c] of lane 16 g + j: rows 4 g .. 4 g + 3 of tile t, column 8 j + c
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < T; ++t) {
       if (t >= nt) break;
       if (t > 0 || r0 > 0) __syncthreads();
 #pragma unroll
       for (int c = 0; c < 8; ++c) sums[wave][c][lane] = acc[t][c];
       __syncthreads();
       // thread -> row 4 rg + ri of the tile and chunk q: neighbours read neighbouring words
-      for (int u = tid; u < 256; u += WAVES * 64) {
+      for (int u = tid; u < 256; u += THREADS) {
         const int q = u & 15, ri = (u >> 4) & 3, rg = u >> 6;
         const int r = r0 + t * 16 + rg * 4 + ri;
         const float* s = (const float*)&sums[0][0][0] + (rg * 16 + q) * 4 + ri;
@@ -416,53 +513,39 @@ __global__ void __launch_bounds__(WAVES * 64, NT == 1 ? 4 : 2) few_kernel(const 
         }
       }
     }
-    if (r0 + 16 * NT < n) __syncthreads();
-  }
-}
-
-// h of the rows from the gate/up parts (where K was split), in two bf16 halves
-__global__ void __launch_bounds__(256) few_swiglu_kernel(const float* __restrict__ part, const int* __restrict__ ids,
-                                                         int splits, int P, int E, int I, uint16_t* __restrict__ h) {
-  const int64_t per = I / 8, t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (t >= P * per) return;
-  const int p = (int)(t / per), c0 = (int)(t % per) * 8;
-  if ((unsigned)ids[p] >= (unsigned)E) return;
-  float l[8] = {}, g[8] = {};
-  for (int s = 0; s < splits; ++s) {
-    const float* q = part + ((int64_t)s * P + p) * 2 * I + c0;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      l[c] += q[c];
-      g[c] += q[I + c];
-    }
-  }
-  uint16_t* hp = h + (int64_t)p * I + c0;
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const float hv = swg::swiglu_h(l[c], g[c]);
-    const bf16_t top = (bf16_t)hv;
-    hp[c] = __builtin_bit_cast(uint16_t, top);
-    hp[(int64_t)P * I + c] = __builtin_bit_cast(uint16_t, (bf16_t)(hv - (float)top));
+  };
+  for (int r0 = 0; r0 < n; r0 += 16 * NT) {
+    if (NT == 1 || n - r0 <= 16) pass(int_c<1>{}, r0);
+    else if (NT == 2 || n - r0 <= 32) pass(int_c<(NT > 1 ? 2 : 1)>{}, r0);
+    else pass(int_c<NT>{}, r0);
   }
 }
 
 // y[m] = rn(sum over the choices j of weights[m,j] times the sum of the row's
-// parts).  A choice whose id names no expert adds nothing.
-__global__ void __launch_bounds__(256) few_combine_kernel(const float* __restrict__ part, const int* __restrict__ ids,
-                                                          const float* __restrict__ weights, int splits, int M, int E,
-                                                          int k, int N, uint16_t* __restrict__ y) {
-  const int64_t per = N / 4, t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+// parts).  A choice whose id names no expert adds nothing (its part was never
+// written: whatever is there is not used).  Eight terms are loaded at a time.
+__global__ void __launch_bounds__(64) few_combine_kernel(const float* __restrict__ part, const int* __restrict__ ids,
+                                                         const float* __restrict__ weights, int splits, int M, int E,
+                                                         int k, int N, uint16_t* __restrict__ y) {
+  const int64_t per = N / 4, t = (int64_t)blockIdx.x * 64 + threadIdx.x;
   if (t >= M * per) return;
-  const int m = (int)(t / per), c0 = (int)(t % per) * 4;
+  const int m = (int)(t / per), c0 = (int)(t % per) * 4, terms = k * splits;
   f32x4 v = {};
-  for (int j = 0; j < k; ++j) {
-    const int p = m * k + j;
-    if ((unsigned)ids[p] >= (unsigned)E) continue;
-    f32x4 s = *(const f32x4*)(part + (int64_t)p * N + c0);
-    for (int q = 1; q < splits; ++q) s += *(const f32x4*)(part + ((int64_t)q * M * k + p) * N + c0);
-    const float w = weights[p];
+  for (int q0 = 0; q0 < terms; q0 += 8) {
+    f32x4 s[8];
+    float w[8];
+    bool valid[8];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] = __builtin_fmaf(w, s[c], v[c]);
+    for (int u = 0; u < 8; ++u) {
+      const int q = min(q0 + u, terms - 1), j = q / splits, p = m * k + j;
+      s[u] = *(const f32x4*)(part + ((int64_t)(q - j * splits) * M * k + p) * N + c0);
+      w[u] = weights[p];
+      valid[u] = q0 + u < terms && (unsigned)ids[p] < (unsigned)E;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = valid[u] ? __builtin_fmaf(w[u], s[u][c], v[c]) : v[c];
   }
   uint2 o;
   o.x = swg::pack2(v[0], v[1]);
@@ -482,9 +565,9 @@ using namespace swb;
 constexpr int64_t kFewTokens = 64;
 constexpr int64_t kFewDim = (int64_t)1 << 18;  // 1024 rows of h within 2^31 bytes
 constexpr int kUnits = 256;  // compute units of an MI355X
-constexpr int kWaves = 8;
+constexpr int kWaves = 4;
 
-int64_t route_slices(int64_t D) { return D / kRouteSlice; }
+int64_t route_slices(int64_t D) { return (D + kRouteSlice - 1) / kRouteSlice; }
 
 // Parts of K: so many that the launch has a workgroup for every compute unit
 // when every slot has its expert, but at least a step of 32 for every wave.
@@ -496,19 +579,24 @@ int few_splits(int64_t blocks, int64_t slots, int64_t K) {
 }
 
 struct Plan {
-  int64_t P, slots;
-  int s1, s2;                      // parts of D in the gate/up, of I in the down product
-  size_t route, h, part1, part2;   // bytes
+  int64_t P, slots, blocks2;
+  int s1, s2;              // parts of D in the gate/up, of I in the down product
+  size_t h, part1, part2;  // bytes
+  size_t bytes() const { return h + part1 + part2; }
 };
 
 Plan plan_few(int64_t M, int64_t D, int64_t I, int64_t Dout, int64_t E, int64_t k) {
   Plan p{};
   p.P = M * k;
   p.slots = p.P < E ? p.P : E;
+  p.blocks2 = (Dout + 127) / 128;
   if (p.P == 0) return p;
   p.s1 = few_splits(I / 64, p.slots, D);
-  p.s2 = few_splits((Dout + 127) / 128, p.slots, I);
-  p.h = align256((size_t)(2 * p.P * I * 2));
+  p.s2 = few_splits(p.blocks2, p.slots, I);
+  // a split gate/up leaves h to the down launch: its rows have to fit there
+  const int64_t width = ((I / 32 + p.s2 - 1) / p.s2) * 32;
+  if (p.P > kPartRows || p.P * width > kPartValues) p.s1 = 1;
+  p.h = p.s1 > 1 ? 0 : align256((size_t)(2 * p.P * I * 2));
   p.part1 = p.s1 > 1 ? align256((size_t)(p.s1 * p.P * 2 * I * 4)) : 0;
   p.part2 = align256((size_t)(p.s2 * p.P * Dout * 4));
   return p;
@@ -537,34 +625,55 @@ int check_few(int64_t M, int64_t D, int64_t I, int64_t Dout, int64_t E, int64_t 
 
 size_t route_bytes(int64_t M, int64_t D, int64_t E) { return align256((size_t)(route_slices(D) * M * E * 8)); }
 
-int run_route(const void* x, const void* wr, int* ids, float* weights, void* ws, int64_t M, int64_t D, int64_t E,
-              int64_t k, int renorm, hipStream_t st) {
-  const int slices = (int)route_slices(D);
-  hipLaunchKernelGGL(route_logits_kernel, dim3((unsigned)slices, (unsigned)((M + 15) / 16), (unsigned)((E + 15) / 16)),
-                     dim3(64), 0, st, (const uint16_t*)x, (const uint16_t*)wr, (double*)ws, (int)M, (int)D, (int)E);
-  SW_TRY(launch_status());
-  hipLaunchKernelGGL(route_topk_kernel, dim3((unsigned)M), dim3(256), 0, st, (const double*)ws, slices, (int)E, (int)k,
-                     renorm, ids, weights);
+int run_logits(const void* x, const void* wr, void* part, int64_t M, int64_t D, int64_t E, hipStream_t st) {
+  hipLaunchKernelGGL(route_logits_kernel,
+                     dim3((unsigned)route_slices(D), (unsigned)((M + 15) / 16), (unsigned)((E + 15) / 16)),
+                     dim3(kRouteWaves * 64), 0, st, (const uint16_t*)x, (const uint16_t*)wr, (double*)part, (int)M, (int)D, (int)E);
+  return launch_status();
+}
+int run_topk(const void* part, int* ids, float* weights, int64_t M, int64_t D, int64_t E, int64_t k, int renorm,
+             hipStream_t st) {
+  hipLaunchKernelGGL(route_topk_kernel, dim3((unsigned)M), dim3(256), 0, st, (const double*)part, (int)route_slices(D),
+                     (int)E, (int)k, renorm, ids, weights);
   return launch_status();
 }
 
-template <int NT, bool GATE>
-int run_few(const FewArgs& a, int64_t slots, hipStream_t st) {
-  const dim3 grid(GATE ? (unsigned)(a.N / 128) : (unsigned)((a.N + 127) / 128), (unsigned)slots, (unsigned)a.splits);
-  if (a.P <= 64) hipLaunchKernelGGL((few_kernel<NT, kWaves, GATE, true>), grid, dim3(kWaves * 64), 0, st, a);
-  else hipLaunchKernelGGL((few_kernel<NT, kWaves, GATE, false>), grid, dim3(kWaves * 64), 0, st, a);
+template <int NT, Kind KIND, int AHEAD>
+int few_launch(const FewArgs& a, const dim3& grid, hipStream_t st) {
+  const dim3 block(kWaves * 64);
+  if constexpr (KIND == kGate || KIND == kDown) {
+    if (a.P > 64) {
+      hipLaunchKernelGGL((few_kernel<NT, kWaves, KIND, false, AHEAD>), grid, block, 0, st, a);
+      return launch_status();
+    }
+  }
+  hipLaunchKernelGGL((few_kernel<NT, kWaves, KIND, true, AHEAD>), grid, block, 0, st, a);
   return launch_status();
 }
-template <bool GATE>
-int run_few(const FewArgs& a, int64_t M, int64_t slots, hipStream_t st) {
-  if (M <= 16) return run_few<1, GATE>(a, slots, st);
-  if (M <= 32) return run_few<2, GATE>(a, slots, st);
-  return run_few<4, GATE>(a, slots, st);
+// Steps in flight: four where a wave has at least eight and its registers hold
+// them (one tile of rows), else two.  60 experts of 2048 x 1024: 83 -> 79 us; with
+// four steps to a wave or two tiles 1 to 4% slower.
+template <int NT, Kind KIND>
+int few_go(const FewArgs& a, const dim3& grid, hipStream_t st) {
+  if (NT == 1 && a.K / 32 >= 8 * kWaves * a.splits) return few_launch<NT, KIND, NT == 1 ? 4 : 2>(a, grid, st);
+  return few_launch<NT, KIND, 2>(a, grid, st);
+}
+template <Kind KIND>
+int few_tokens(const FewArgs& a, int64_t M, const dim3& grid, hipStream_t st) {
+  if (M <= 16) return few_go<1, KIND>(a, grid, st);
+  if (M <= 32) return few_go<2, KIND>(a, grid, st);
+  return few_go<4, KIND>(a, grid, st);
 }
 
-int run_experts(const void* x, const void* W1, const void* W_down, const int* ids, const float* weights, void* y,
-                void* ws, const Plan& pl, int64_t M, int64_t D, int64_t I, int64_t Dout, int64_t E, int64_t k,
-                hipStream_t st) {
+// Whether the gate/up launch ranks the logits itself: a choice of up to 64 pairs
+// out of up to 256 logits.
+bool route_inline(int64_t M, int64_t E, int64_t k) { return M * E <= kRouteInline && M * k <= 64; }
+
+// logits: the router's slices where the gate/up launch makes ids and weights of
+// them; NULL where these are given.
+int run_experts(const void* x, const void* W1, const void* W_down, int* ids, float* weights, const void* logits,
+                int renorm, void* y, void* ws, const Plan& pl, int64_t M, int64_t D, int64_t I, int64_t Dout, int64_t E,
+                int64_t k, hipStream_t st) {
   char* w = (char*)ws;
   uint16_t* h = (uint16_t*)w;
   float* part1 = (float*)(w + pl.h);
@@ -573,6 +682,7 @@ int run_experts(const void* x, const void* W1, const void* W_down, const int* id
   a.x = (const uint16_t*)x;
   a.w = (const uint16_t*)W1;
   a.ids = ids;
+  a.weights = weights;
   a.part = part1;
   a.h = h;
   a.P = (int)pl.P;
@@ -581,22 +691,24 @@ int run_experts(const void* x, const void* W1, const void* W_down, const int* id
   a.K = (int)D;
   a.N = (int)(2 * I);
   a.splits = pl.s1;
-  SW_TRY(run_few<true>(a, M, pl.slots, st));
-  if (pl.s1 > 1) {
-    hipLaunchKernelGGL(few_swiglu_kernel, dim3((unsigned)((pl.P * (I / 8) + 255) / 256)), dim3(256), 0, st,
-                       (const float*)part1, ids, pl.s1, (int)pl.P, (int)E, (int)I, h);
-    SW_TRY(launch_status());
-  }
+  a.logits = (const double*)logits;
+  a.slices = (int)route_slices(D);
+  a.renorm = renorm;
+  const dim3 gate_grid((unsigned)(I / 64), (unsigned)pl.slots, (unsigned)pl.s1);
+  SW_TRY(logits ? few_tokens<kGateRoute>(a, M, gate_grid, st) : few_tokens<kGate>(a, M, gate_grid, st));
   a.x = h;
   a.w = (const uint16_t*)W_down;
   a.part = part2;
-  a.h = nullptr;
   a.K = (int)I;
   a.N = (int)Dout;
   a.splits = pl.s2;
-  SW_TRY(run_few<false>(a, M, pl.slots, st));
-  hipLaunchKernelGGL(few_combine_kernel, dim3((unsigned)((M * (Dout / 4) + 255) / 256)), dim3(256), 0, st,
-                     (const float*)part2, ids, weights, pl.s2, (int)M, (int)E, (int)k, (int)Dout, (uint16_t*)y);
+  a.gate_part = part1;
+  a.gate_splits = pl.s1;
+  const dim3 down_grid((unsigned)pl.blocks2, (unsigned)pl.slots, (unsigned)pl.s2);
+  SW_TRY((pl.s1 > 1 ? few_go<1, kDownPart>(a, down_grid, st) : few_tokens<kDown>(a, M, down_grid, st)));
+  hipLaunchKernelGGL(few_combine_kernel, dim3((unsigned)((M * (Dout / 4) + 63) / 64)), dim3(64), 0, st,
+                     (const float*)part2, (const int*)ids, (const float*)weights, pl.s2, (int)M, (int)E, (int)k,
+                     (int)Dout, (uint16_t*)y);
   return launch_status();
 }
 
@@ -623,14 +735,15 @@ int swiglu_moe_route(const void* x, const void* W_router, int32_t* ids, float* w
   const Range outs[] = {rng(ids, M * k * 4), rng(weights, M * k * 4), rng(ws, (int64_t)need)};
   SW_TRY(check_alias(ins, 2, outs, 3));
   if (M == 0) return SWIGLU_OK;
-  return run_route(x, W_router, ids, weights, ws, M, D, E, k, renormalize ? 1 : 0, as_stream(stream));
+  hipStream_t st = as_stream(stream);
+  SW_TRY(run_logits(x, W_router, ws, M, D, E, st));
+  return run_topk(ws, ids, weights, M, D, E, k, renormalize ? 1 : 0, st);
 }
 
-// h, the gate/up parts, the down parts
+// h or the gate/up parts, the down parts
 size_t swiglu_moe_few_workspace(int64_t M, int64_t D, int64_t I, int64_t Dout, int64_t E, int64_t k) {
   if (check_few(M, D, I, Dout, E, k) != SWIGLU_OK) return 0;
-  const Plan p = plan_few(M, D, I, Dout, E, k);
-  return p.h + p.part1 + p.part2;
+  return plan_few(M, D, I, Dout, E, k).bytes();
 }
 
 int swiglu_moe_few_fwd(const void* x, const void* W1, const void* W_down, const int32_t* ids, const float* weights,
@@ -642,14 +755,15 @@ int swiglu_moe_few_fwd(const void* x, const void* W1, const void* W_down, const 
       !aligned_to(weights, 4) || !aligned_to(y, 16) || !aligned_to(ws, 16))
     return SWIGLU_ERR_ALIGN;
   const Plan pl = plan_few(M, D, I, Dout, E, k);
-  const size_t need = pl.h + pl.part1 + pl.part2;
+  const size_t need = pl.bytes();
   if (need > 0 && (!ws || ws_bytes < need)) return SWIGLU_ERR_WORKSPACE;
   const Range ins[] = {rng(x, M * D * 2), rng(W1, E * D * 2 * I * 2), rng(W_down, E * I * Dout * 2),
                        rng(ids, M * k * 4), rng(weights, M * k * 4)};
   const Range outs[] = {rng(y, M * Dout * 2), rng(ws, (int64_t)need)};
   SW_TRY(check_alias(ins, 5, outs, 2));
   if (M == 0) return SWIGLU_OK;
-  return run_experts(x, W1, W_down, ids, weights, y, ws, pl, M, D, I, Dout, E, k, as_stream(stream));
+  return run_experts(x, W1, W_down, const_cast<int32_t*>(ids), const_cast<float*>(weights), nullptr, 0, y, ws, pl, M, D,
+                     I, Dout, E, k, as_stream(stream));
 }
 
 size_t swiglu_moe_few_layer_workspace(int64_t M, int64_t D, int64_t I, int64_t Dout, int64_t E, int64_t k) {
@@ -667,7 +781,7 @@ int swiglu_moe_few_layer(const void* x, const void* W_router, const void* W1, co
       !aligned_to(ids, 4) || !aligned_to(weights, 4) || !aligned_to(y, 16) || !aligned_to(ws, 16))
     return SWIGLU_ERR_ALIGN;
   const Plan pl = plan_few(M, D, I, Dout, E, k);
-  const size_t own = pl.h + pl.part1 + pl.part2, need = own + route_bytes(M, D, E);
+  const size_t own = pl.bytes(), need = own + route_bytes(M, D, E);
   if (need > 0 && (!ws || ws_bytes < need)) return SWIGLU_ERR_WORKSPACE;
   const Range ins[] = {rng(x, M * D * 2), rng(W_router, D * E * 2), rng(W1, E * D * 2 * I * 2),
                        rng(W_down, E * I * Dout * 2)};
@@ -675,8 +789,12 @@ int swiglu_moe_few_layer(const void* x, const void* W_router, const void* W1, co
   SW_TRY(check_alias(ins, 4, outs, 4));
   if (M == 0) return SWIGLU_OK;
   hipStream_t st = as_stream(stream);
-  SW_TRY(run_route(x, W_router, ids, weights, (char*)ws + own, M, D, E, k, renormalize ? 1 : 0, st));
-  return run_experts(x, W1, W_down, ids, weights, y, ws, pl, M, D, I, Dout, E, k, st);
+  void* logits = (char*)ws + own;
+  SW_TRY(run_logits(x, W_router, logits, M, D, E, st));
+  const bool inl = route_inline(M, E, k);
+  if (!inl) SW_TRY(run_topk(logits, ids, weights, M, D, E, k, renormalize ? 1 : 0, st));
+  return run_experts(x, W1, W_down, ids, weights, inl ? logits : nullptr, renormalize ? 1 : 0, y, ws, pl, M, D, I, Dout,
+                     E, k, st);
 }
 
 }  // extern "C"
