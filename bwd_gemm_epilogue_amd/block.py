@@ -1,7 +1,12 @@
 """Binding of include/swiglu_block.h: the operators around the SwiGLU MLP step
 in a block that trains or serves it.  As in the rest of the package every
 function marshals arguments only; the arithmetic runs in the HIP kernels and
-there is no CPU path."""
+there is no CPU path.
+
+The regular case of each short call goes through the native half of the
+binding (csrc/host.cpp), which checks, allocates and launches at a fraction of
+the cost; what it does not take comes back as None and is done, or refused,
+here."""
 from __future__ import annotations
 
 import ctypes
@@ -9,7 +14,7 @@ import math
 
 import torch
 
-from . import _check, _launches, _on_gpu, _stream, _ws, lib
+from . import SwiGLUError, _check, _launches, _on_gpu, _stream, _ws, lib
 
 __all__ = [
     "swiglu_layer_norm_fwd", "swiglu_layer_norm_bwd", "swiglu_layer_norm_bwd_workspace",
@@ -28,6 +33,25 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     if code is None:
         raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
     return code
+
+
+_module = None
+
+
+def _host():
+    """The native half of the binding (raises if it has not been built)."""
+    global _module
+    if _module is None:
+        lib()
+        from . import _host as _module
+    return _module
+
+
+def _native(fn: str, got):
+    """A result of the native half: a status is an error."""
+    if type(got) is int:
+        raise SwiGLUError(fn, got)
+    return got
 
 
 # These calls are short, so the checks are written to cost little when they
@@ -81,6 +105,10 @@ def swiglu_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None
     """y = (x - mean) rstd weight + bias over the last dimension of x [M,D]
     (dense rows, any row stride): returns (y, mean, rstd), the statistics
     float32 [M]."""
+    if y is None and mean is None and rstd is None:
+        got = _host().layer_norm_fwd(x, weight, bias, eps, _stream(x, stream))
+        if got is not None:
+            return _native("swiglu_layer_norm_fwd", got)
     if x.dim() != 2:
         raise ValueError(f"x must have two dimensions, got {tuple(x.shape)}")
     shape, t, dev = x.shape, x.dtype, x.get_device()
@@ -114,6 +142,10 @@ def swiglu_layer_norm_bwd(dy, x, weight, mean, rstd, dres=None, bias_grad=True, 
     added to dx (the gradient that reaches x by a residual branch).  dweight
     is None where weight is; dbias is None unless bias_grad (its type is the
     weight's, or x's where there is none)."""
+    if dx is None and dweight is None and dbias is None and ws is None:
+        got = _host().layer_norm_bwd(dy, x, weight, mean, rstd, dres, bias_grad, _stream(x, stream))
+        if got is not None:
+            return _native("swiglu_layer_norm_bwd", got)
     if x.dim() != 2:
         raise ValueError(f"x must have two dimensions, got {tuple(x.shape)}")
     shape, t, dev = x.shape, x.dtype, x.get_device()
@@ -204,6 +236,10 @@ def _addresses(tensors, name: str, dev: int):
 
 
 def _clip(grads, max_norm, outs, total, ws, stream):
+    if total is None and ws is None and not isinstance(grads, torch.Tensor):
+        got = _host().clip_grad_norm(grads, outs, float(max_norm), _stream(None, stream))
+        if got is not None:
+            return _native("swiglu_clip_grad_norm", got)
     if isinstance(grads, torch.Tensor):
         grads, outs = [grads], None if outs is None else [outs]
     if outs is not None and len(outs) != len(grads):
@@ -303,6 +339,10 @@ def swiglu_moe_few_fwd(x, W1, W_down, ids, weights, y=None, ws=None, stream=None
     """y[m] = sum_j weights[m,j] MLP_{ids[m,j]}(x[m]) for up to 64 tokens: x
     [M,D], W1 [E,D,2I], W_down [E,I,Dout], ids int32 [M,k], weights float32
     [M,k].  An id outside [0, E) adds nothing."""
+    if y is None and ws is None:
+        got = _host().moe_few(x, None, W1, W_down, ids, weights, _stream(x, stream))
+        if got is not None:
+            return _native("swiglu_moe_few_fwd", got)
     dev = x.get_device()
     xp = _typed(x, "x", x.shape, _BF16, dev)
     M, D, I, Dout, E, w1p, wdp = _experts(x, W1, W_down, dev)
@@ -321,6 +361,10 @@ def swiglu_moe_few_layer(x, W_router, W1, W_down, k, renormalize=True, y=None, i
                          stream=None):
     """The whole layer for up to 64 tokens, router and experts: (y [M,Dout],
     ids int32 [M,k], weights float32 [M,k])."""
+    if y is None and ids is None and weights is None and ws is None:
+        got = _host().moe_few(x, W_router, W1, W_down, k, bool(renormalize), _stream(x, stream))
+        if got is not None:
+            return _native("swiglu_moe_few_layer", got)
     dev = x.get_device()
     xp = _typed(x, "x", x.shape, _BF16, dev)
     M, D, I, Dout, E, w1p, wdp = _experts(x, W1, W_down, dev)

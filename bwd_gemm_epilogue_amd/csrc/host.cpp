@@ -1,0 +1,258 @@
+// host.cpp -- the host's part of the short calls of include/swiglu_block.h, in
+// native code: a one-token layer norm or a clip of hundreds of small gradients
+// costs more in marshalling than on the GPU (through ctypes 13 us and 144 us).
+//
+// Every function here takes the regular case of its namesake in block.py:
+// tensors of the right types, shapes and layout on one GPU, outputs to be
+// allocated.  It returns the result, or the negative status of a call that
+// failed, or None for anything else, which block.py then does, or words the
+// refusal of, in the general way.
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+#include <ATen/ATen.h>
+
+#include <vector>
+
+#include "swiglu_block.h"
+
+namespace {
+
+using at::Tensor;
+
+PyObject* none() { Py_RETURN_NONE; }
+
+int dtype_of(const Tensor& t) {
+  switch (t.scalar_type()) {
+    case at::kBFloat16: return SWIGLU_BF16;
+    case at::kHalf: return SWIGLU_FP16;
+    case at::kFloat: return SWIGLU_FP32;
+    default: return -1;
+  }
+}
+
+// a plain tensor in GPU memory (dev < 0: any GPU)
+bool plain(PyObject* o, int64_t dev) {
+  if (!THPVariable_Check(o)) return false;
+  const Tensor& t = THPVariable_Unpack(o);
+  return t.defined() && t.is_cuda() && t.layout() == at::kStrided && !t.key_set().has(c10::DispatchKey::Python) &&
+         !t.is_neg() && t.has_storage() && (dev < 0 || t.get_device() == dev);
+}
+
+struct Rows {
+  void* p = nullptr;
+  int64_t ld = 0;
+};
+// a matrix of dense, separate rows of this type
+bool rows_of(PyObject* o, at::ScalarType type, int64_t M, int64_t D, int64_t dev, Rows* r) {
+  if (!plain(o, dev)) return false;
+  const Tensor& t = THPVariable_Unpack(o);
+  if (t.scalar_type() != type || t.dim() != 2 || t.size(0) != M || t.size(1) != D) return false;
+  if (D > 1 && M > 0 && t.stride(1) != 1) return false;
+  r->ld = M > 1 ? t.stride(0) : D;
+  r->p = t.data_ptr();
+  return r->ld >= D;
+}
+// a contiguous tensor of this type and shape
+bool dense_of(PyObject* o, at::ScalarType type, at::IntArrayRef shape, int64_t dev, void** p) {
+  if (!plain(o, dev)) return false;
+  const Tensor& t = THPVariable_Unpack(o);
+  if (t.scalar_type() != type || t.sizes() != shape || !t.is_contiguous()) return false;
+  *p = t.data_ptr();
+  return true;
+}
+// None, or a weight of x's type or float32: every one that is given of one type
+bool vector_of(PyObject* o, int64_t D, int64_t dev, at::ScalarType x, at::ScalarType* type, bool* given, void** p) {
+  *p = nullptr;
+  if (o == Py_None) return true;
+  if (!plain(o, dev)) return false;
+  const Tensor& t = THPVariable_Unpack(o);
+  if (!*given) {
+    *type = t.scalar_type();
+    *given = true;
+    if (*type != x && *type != at::kFloat) return false;
+  }
+  return dense_of(o, *type, {D}, dev, p);
+}
+
+Tensor workspace(size_t bytes, const Tensor& like) {
+  return at::empty({(int64_t)(bytes > 0 ? bytes : 1)}, like.options().dtype(at::kByte));
+}
+
+PyObject* pack(std::initializer_list<Tensor> ts) {
+  PyObject* out = PyTuple_New((Py_ssize_t)ts.size());
+  if (!out) return nullptr;
+  Py_ssize_t i = 0;
+  for (const Tensor& t : ts) {
+    PyObject* v = nullptr;
+    if (t.defined()) {
+      v = THPVariable_Wrap(t);
+    } else {
+      Py_INCREF(Py_None);
+      v = Py_None;
+    }
+    if (!v) {
+      Py_DECREF(out);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(out, i++, v);
+  }
+  return out;
+}
+
+void* stream_of(PyObject* o) { return PyLong_AsVoidPtr(o); }
+
+// (x, weight, bias, eps, stream)
+PyObject* layer_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 5 || !plain(a[0], -1)) return none();
+  const Tensor& x = THPVariable_Unpack(a[0]);
+  const int dt = dtype_of(x);
+  if (x.dim() != 2 || dt < 0 || !PyFloat_CheckExact(a[3])) return none();
+  const int64_t M = x.size(0), D = x.size(1), dev = x.get_device();
+  Rows xr;
+  at::ScalarType wt = x.scalar_type();
+  bool given = false;
+  void *w, *b;
+  if (!rows_of(a[0], x.scalar_type(), M, D, dev, &xr) || !vector_of(a[1], D, dev, x.scalar_type(), &wt, &given, &w) ||
+      !vector_of(a[2], D, dev, x.scalar_type(), &wt, &given, &b))
+    return none();
+  Tensor y = at::empty({M, D}, x.options());
+  Tensor mean = at::empty({M}, x.options().dtype(at::kFloat)), rstd = at::empty({M}, mean.options());
+  const int s = swiglu_layer_norm_fwd(xr.p, xr.ld, w, b, y.data_ptr(), D, (float*)mean.data_ptr(),
+                                      (float*)rstd.data_ptr(), M, D, PyFloat_AS_DOUBLE(a[3]), dt,
+                                      wt == at::kFloat ? SWIGLU_FP32 : dt, stream_of(a[4]));
+  return s == SWIGLU_OK ? pack({y, mean, rstd}) : PyLong_FromLong(s);
+  END_HANDLE_TH_ERRORS
+}
+
+// (dy, x, weight, mean, rstd, dres, bias_grad, stream)
+PyObject* layer_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 8 || !plain(a[1], -1)) return none();
+  const Tensor& x = THPVariable_Unpack(a[1]);
+  const int dt = dtype_of(x);
+  if (x.dim() != 2 || dt < 0 || (a[6] != Py_True && a[6] != Py_False)) return none();
+  const int64_t M = x.size(0), D = x.size(1), dev = x.get_device();
+  const bool bias = a[6] == Py_True;
+  Rows dyr, xr, rr;
+  at::ScalarType wt = x.scalar_type();
+  bool given = false;
+  void *w, *mean, *rstd;
+  if (!rows_of(a[0], x.scalar_type(), M, D, dev, &dyr) || !rows_of(a[1], x.scalar_type(), M, D, dev, &xr) ||
+      !vector_of(a[2], D, dev, x.scalar_type(), &wt, &given, &w) || !dense_of(a[3], at::kFloat, {M}, dev, &mean) ||
+      !dense_of(a[4], at::kFloat, {M}, dev, &rstd))
+    return none();
+  if (a[5] != Py_None && !rows_of(a[5], x.scalar_type(), M, D, dev, &rr)) return none();
+  Tensor dx = at::empty({M, D}, x.options()), dw, db;
+  if (w) dw = at::empty({D}, x.options().dtype(wt));
+  if (bias) db = at::empty({D}, x.options().dtype(wt));
+  const size_t need = w || bias ? swiglu_layer_norm_bwd_workspace(M, D) : 0;
+  const Tensor ws = workspace(need, x);
+  const int s = swiglu_layer_norm_bwd(dyr.p, dyr.ld, xr.p, xr.ld, w, (const float*)mean, (const float*)rstd, rr.p,
+                                      rr.p ? rr.ld : D, dx.data_ptr(), D, w ? dw.data_ptr() : nullptr,
+                                      bias ? db.data_ptr() : nullptr, ws.data_ptr(), (size_t)ws.numel(), M, D, dt,
+                                      wt == at::kFloat ? SWIGLU_FP32 : dt, stream_of(a[7]));
+  return s == SWIGLU_OK ? pack({dx, dw, db}) : PyLong_FromLong(s);
+  END_HANDLE_TH_ERRORS
+}
+
+// (grads, outs, max_norm, stream): lists or tuples of tensors
+PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 4 || !(PyList_CheckExact(a[0]) || PyTuple_CheckExact(a[0])) || !PyFloat_CheckExact(a[2])) return none();
+  const bool apart = a[1] != Py_None;
+  if (apart && !(PyList_CheckExact(a[1]) || PyTuple_CheckExact(a[1]))) return none();
+  const Py_ssize_t count = PySequence_Fast_GET_SIZE(a[0]);
+  if (count == 0 || (apart && PySequence_Fast_GET_SIZE(a[1]) != count)) return none();
+  PyObject** grads = PySequence_Fast_ITEMS(a[0]);
+  PyObject** outs = apart ? PySequence_Fast_ITEMS(a[1]) : nullptr;
+  if (!plain(grads[0], -1)) return none();
+  const Tensor& like = THPVariable_Unpack(grads[0]);
+  const int64_t dev = like.get_device();
+  std::vector<const void*> g((size_t)count);
+  std::vector<void*> o((size_t)(apart ? count : 0));
+  std::vector<int64_t> numel((size_t)count);
+  std::vector<int> types((size_t)count);
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    if (!plain(grads[i], dev)) return none();
+    const Tensor& t = THPVariable_Unpack(grads[i]);
+    const int dt = dtype_of(t);
+    if (dt < 0 || !t.is_contiguous()) return none();
+    g[i] = t.data_ptr();
+    numel[i] = t.numel();
+    types[i] = dt;
+    if (apart) {
+      if (!plain(outs[i], dev)) return none();
+      const Tensor& u = THPVariable_Unpack(outs[i]);
+      if (u.scalar_type() != t.scalar_type() || u.numel() != t.numel() || !u.is_contiguous()) return none();
+      o[i] = u.data_ptr();
+    }
+  }
+  Tensor total = at::empty({}, like.options().dtype(at::kFloat));
+  const Tensor ws = workspace(swiglu_clip_grad_norm_workspace(count), like);
+  const int s = swiglu_clip_grad_norm(g.data(), apart ? o.data() : nullptr, numel.data(), types.data(), count,
+                                      PyFloat_AS_DOUBLE(a[2]), (float*)total.data_ptr(), ws.data_ptr(),
+                                      (size_t)ws.numel(), stream_of(a[3]));
+  return s == SWIGLU_OK ? THPVariable_Wrap(total) : PyLong_FromLong(s);
+  END_HANDLE_TH_ERRORS
+}
+
+// (x, W_router or None, W1, W_down, k or ids, renormalize or weights, stream): the
+// whole layer, or the experts alone where W_router is None
+PyObject* moe_few(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 7 || !plain(a[0], -1) || !THPVariable_Check(a[3])) return none();
+  const Tensor& x = THPVariable_Unpack(a[0]);
+  const Tensor& wd = THPVariable_Unpack(a[3]);
+  if (x.dim() != 2 || wd.dim() != 3) return none();
+  const int64_t M = x.size(0), D = x.size(1), dev = x.get_device();
+  const int64_t E = wd.size(0), I = wd.size(1), Dout = wd.size(2);
+  void *xp, *w1, *w2, *wr = nullptr, *ip = nullptr, *gp = nullptr;
+  if (!dense_of(a[0], at::kBFloat16, {M, D}, dev, &xp) || !dense_of(a[2], at::kBFloat16, {E, D, 2 * I}, dev, &w1) ||
+      !dense_of(a[3], at::kBFloat16, {E, I, Dout}, dev, &w2))
+    return none();
+  const bool route = a[1] != Py_None;
+  Tensor ids, weights;
+  int64_t k;
+  if (route) {
+    if (!dense_of(a[1], at::kBFloat16, {D, E}, dev, &wr) || !PyLong_CheckExact(a[4]) ||
+        (a[5] != Py_True && a[5] != Py_False))
+      return none();
+    k = PyLong_AsLongLong(a[4]);
+    if (k < 1 || k > E) {  // worded by the general way
+      PyErr_Clear();
+      return none();
+    }
+    ids = at::empty({M, k}, x.options().dtype(at::kInt));
+    weights = at::empty({M, k}, x.options().dtype(at::kFloat));
+    ip = ids.data_ptr();
+    gp = weights.data_ptr();
+  } else {
+    if (!plain(a[4], dev) || THPVariable_Unpack(a[4]).dim() != 2) return none();
+    k = THPVariable_Unpack(a[4]).size(1);
+    if (!dense_of(a[4], at::kInt, {M, k}, dev, &ip) || !dense_of(a[5], at::kFloat, {M, k}, dev, &gp)) return none();
+  }
+  Tensor y = at::empty({M, Dout}, x.options());
+  const Tensor ws = workspace(route ? swiglu_moe_few_layer_workspace(M, D, I, Dout, E, k)
+                                    : swiglu_moe_few_workspace(M, D, I, Dout, E, k), x);
+  void* st = stream_of(a[6]);
+  const int s = route ? swiglu_moe_few_layer(xp, wr, w1, w2, y.data_ptr(), (int32_t*)ip, (float*)gp, ws.data_ptr(),
+                                             (size_t)ws.numel(), M, D, I, Dout, E, k, a[5] == Py_True, st)
+                      : swiglu_moe_few_fwd(xp, w1, w2, (const int32_t*)ip, (const float*)gp, y.data_ptr(),
+                                           ws.data_ptr(), (size_t)ws.numel(), M, D, I, Dout, E, k, st);
+  if (s != SWIGLU_OK) return PyLong_FromLong(s);
+  return route ? pack({y, ids, weights}) : THPVariable_Wrap(y);
+  END_HANDLE_TH_ERRORS
+}
+
+PyMethodDef methods[] = {
+    {"layer_norm_fwd", (PyCFunction)(void*)layer_norm_fwd, METH_FASTCALL, nullptr},
+    {"layer_norm_bwd", (PyCFunction)(void*)layer_norm_bwd, METH_FASTCALL, nullptr},
+    {"clip_grad_norm", (PyCFunction)(void*)clip_grad_norm, METH_FASTCALL, nullptr},
+    {"moe_few", (PyCFunction)(void*)moe_few, METH_FASTCALL, nullptr},
+    {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_host", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__host(void) { return PyModule_Create(&module); }
