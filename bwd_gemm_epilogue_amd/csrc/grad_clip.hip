@@ -24,6 +24,7 @@ constexpr int kTensors = 128;   // of one table: 29 bytes each within 4 KB of ar
 // Workgroups of a pass at most, each with one partial sum.  1024, 2048, 4096:
 // 626, 619, 600 us to clip 1.23 GB.
 constexpr int kGroups = 4096;
+constexpr int kSumParts = 2048;
 
 struct Table {
   const void* in[kTensors];
@@ -133,23 +134,33 @@ __global__ void __launch_bounds__(256) grad_norm_kernel(const Table t, const Tab
   if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
-// total and the factor from the parts, added in a fixed order
-__global__ void __launch_bounds__(1024) grad_total_kernel(const double* __restrict__ part, int parts, double max_norm,
-                                                          float* total, float* factor) {
-  __shared__ double red[16];
-  double v[kGroups / 1024], s = 0.0;
+// The total and the factor from N parts at most, added in a fixed order; by the
+// whole workgroup, the result in every thread.
+struct Clip {
+  double total;
+  float factor;
+};
+template <int THREADS, int N>
+__device__ __forceinline__ Clip clip_of(const double* __restrict__ part, int parts, double max_norm, double* red) {
+  double v[N / THREADS], s = 0.0;
 #pragma unroll
-  for (int u = 0; u < kGroups / 1024; ++u) {
-    const int p = u * 1024 + (int)threadIdx.x;
+  for (int u = 0; u < N / THREADS; ++u) {
+    const int p = u * THREADS + (int)threadIdx.x;
     v[u] = p < parts ? part[p] : 0.0;
   }
 #pragma unroll
-  for (int u = 0; u < kGroups / 1024; ++u) s += v[u];
-  s = group_sum<16>(s, red);
+  for (int u = 0; u < N / THREADS; ++u) s += v[u];
+  s = group_sum<THREADS / 64>(s, red);
+  const double norm = __builtin_sqrt(s), q = max_norm / (norm + 1e-6);
+  return {norm, q < 1.0 || q != q ? (float)q : 1.0f};
+}
+__global__ void __launch_bounds__(1024) grad_total_kernel(const double* __restrict__ part, int parts, double max_norm,
+                                                          float* total, float* factor) {
+  __shared__ double red[16];
+  const Clip c = clip_of<1024, kGroups>(part, parts, max_norm, red);
   if (threadIdx.x == 0) {
-    const double norm = __builtin_sqrt(s), q = max_norm / (norm + 1e-6);
-    *total = (float)norm;
-    *factor = q < 1.0 || q != q ? (float)q : 1.0f;
+    *total = (float)c.total;
+    *factor = c.factor;
   }
 }
 
@@ -181,10 +192,22 @@ __device__ __forceinline__ void scale(const T* p, T* o, int n, float f) {
 // from the first chunk on).  These loads are the gradients' last use and
 // stream past the caches (in place, 308 MB: 187 -> 151 us with chunks of 16384
 // elements; 1.23 GB: 655 -> 626).
-template <bool FAR>
+// SUM: up to kSumParts parts are added by every workgroup for itself, which
+// saves the launch between (the tiny block's four gradients: 14.5 -> 11.0 us).
+template <bool FAR, bool SUM>
 __global__ void __launch_bounds__(256) grad_scale_kernel(const Table t, const Table* ts, int tables, int chunks,
-                                                         const float* __restrict__ factor) {
-  const float f = *factor;
+                                                         const float* __restrict__ factor,
+                                                         const double* __restrict__ part, int parts, double max_norm,
+                                                         float* total) {
+  float f;
+  if constexpr (SUM) {
+    __shared__ double red[4];
+    const Clip c = clip_of<256, kSumParts>(part, parts, max_norm, red);
+    f = c.factor;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *total = (float)c.total;
+  } else {
+    f = *factor;
+  }
   for (int c = (chunks - 1) / (int)gridDim.x * (int)gridDim.x + (int)blockIdx.x; c >= 0; c -= gridDim.x) {
     if (c >= chunks) continue;
     Piece p;
@@ -324,13 +347,17 @@ int swiglu_clip_grad_norm(const void* const* grads, void* const* outs, const int
     hipLaunchKernelGGL(k, dim3((unsigned)groups), dim3(256), 0, st, t, (const Table*)tabs, tables, chunks, part);
     SW_TRY(launch_status());
   }
-  hipLaunchKernelGGL(grad_total_kernel, dim3(1), dim3(1024), 0, st, (const double*)part, groups, max_norm, total,
-                     factor);
-  SW_TRY(launch_status());
-  if (norm_only || groups == 0) return SWIGLU_OK;
-  auto k = tables > 1 ? grad_scale_kernel<true> : grad_scale_kernel<false>;
+  const bool sum = !norm_only && groups > 0 && groups <= kSumParts;
+  if (!sum) {
+    hipLaunchKernelGGL(grad_total_kernel, dim3(1), dim3(1024), 0, st, (const double*)part, groups, max_norm, total,
+                       factor);
+    SW_TRY(launch_status());
+    if (norm_only || groups == 0) return SWIGLU_OK;
+  }
+  auto k = tables > 1 ? (sum ? grad_scale_kernel<true, true> : grad_scale_kernel<true, false>)
+                      : (sum ? grad_scale_kernel<false, true> : grad_scale_kernel<false, false>);
   hipLaunchKernelGGL(k, dim3((unsigned)groups), dim3(256), 0, st, t, (const Table*)tabs, tables, chunks,
-                     (const float*)factor);
+                     (const float*)factor, (const double*)part, groups, max_norm, total);
   return launch_status();
 }
 

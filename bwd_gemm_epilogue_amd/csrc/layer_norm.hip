@@ -522,7 +522,9 @@ int fwd_typed(const FwdArgs& a, hipStream_t st) {
 template <class T, class W, int G, int E, int THREADS, bool AHEAD = true>
 int bwd_go(const BwdArgs& a, int64_t* parts, hipStream_t st) {
   const int64_t blocks = (a.M + THREADS / G - 1) / (THREADS / G);
-  *parts = blocks < kBwdGroups ? blocks : kBwdGroups;
+  // as many workgroups as finish in the same number of rounds
+  const int64_t rounds = (blocks + kBwdGroups - 1) / kBwdGroups;
+  *parts = (blocks + rounds - 1) / rounds;
   hipLaunchKernelGGL((ln_bwd_kernel<T, W, G, E / Vec<T>::N, THREADS, AHEAD>), dim3((unsigned)*parts), dim3(THREADS), 0, st, a);
   return launch_status();
 }
