@@ -14,7 +14,8 @@ import math
 
 import torch
 
-from . import SwiGLUError, _check, _launches, _on_gpu, _stream, _ws, lib
+from . import (SwiGLUError, _check, _launches, _on_gpu, _stream, _ws, lib, swiglu_fwd_down_residual, swiglu_fwd_gemm1,
+               swiglu_mlp_bwd)
 
 __all__ = [
     "swiglu_layer_norm_fwd", "swiglu_layer_norm_bwd", "swiglu_layer_norm_bwd_workspace",
@@ -22,6 +23,7 @@ __all__ = [
     "swiglu_clip_grad_norm", "swiglu_clip_grad_norm_workspace", "swiglu_grad_norm",
     "swiglu_moe_route_workspace", "swiglu_moe_route", "swiglu_moe_few_workspace", "swiglu_moe_few_fwd",
     "swiglu_moe_few_layer_workspace", "swiglu_moe_few_layer",
+    "SwiGLUPreNormMLPFunction", "swiglu_prenorm_mlp",
 ]
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
@@ -186,6 +188,12 @@ def _as_rows(t: torch.Tensor) -> torch.Tensor:
     return t if dense else t.contiguous()
 
 
+def _bias_grad(x, weight, dtype):
+    """A tensor for the bias's gradient where its type is not the one that
+    swiglu_layer_norm_bwd gives it (a bias without a weight)."""
+    return torch.empty(x.shape[1], dtype=dtype, device=x.device) if weight is None else None
+
+
 class SwiGLULayerNormFunction(torch.autograd.Function):
     """Layer norm over the last dimension; saves {x, weight, mean, rstd}."""
 
@@ -202,7 +210,7 @@ class SwiGLULayerNormFunction(torch.autograd.Function):
     def backward(ctx, grad_y):
         x2, weight, mean, rstd = ctx.saved_tensors
         _, need_w, need_b, _ = ctx.needs_input_grad
-        dbias = torch.empty(x2.shape[1], dtype=ctx.bias_type, device=x2.device) if need_b else None
+        dbias = _bias_grad(x2, weight, ctx.bias_type) if need_b else None
         dx, dw, db = swiglu_layer_norm_bwd(_as_rows(grad_y), x2, weight, mean, rstd, bias_grad=need_b, dbias=dbias)
         return dx.reshape(ctx.shape), dw if need_w else None, db, None
 
@@ -378,3 +386,40 @@ def swiglu_moe_few_layer(x, W_router, W1, W_down, k, renormalize=True, y=None, i
         _typed(weights, "weights", (M, k), _F32, dev), ws.data_ptr(), ws.numel() * ws.element_size(),
         M, D, I, Dout, E, k, bool(renormalize), _stream(x, stream)))
     return y, ids, weights
+
+
+# --------------------------------------------------------------------------
+# the block they make with the MLP step
+# --------------------------------------------------------------------------
+
+class SwiGLUPreNormMLPFunction(torch.autograd.Function):
+    """y = x + MLP(norm(x)), the MLP half of a pre-norm block.
+
+    Forward: layer norm, GEMM-1 with its SwiGLU epilogue, the down GEMM with x
+    added in its epilogue.  Backward: swiglu_mlp_bwd, then the norm's backward
+    with the residual branch's gradient joining dx.  Saves {x, norm weight,
+    mean, rstd, norm(x), W1, W_down, preact}."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, W1, W_down, eps):
+        x2 = x.reshape(-1, x.shape[-1]).contiguous()
+        normed, mean, rstd = swiglu_layer_norm_fwd(x2, weight, bias, eps)
+        preact, h = swiglu_fwd_gemm1(normed, W1.contiguous())
+        y = swiglu_fwd_down_residual(h, W_down.contiguous(), x2)
+        ctx.save_for_backward(x2, weight, mean, rstd, normed, W1, W_down, preact)
+        ctx.bias_type = None if bias is None else bias.dtype
+        return y.reshape(x.shape)
+
+    @staticmethod
+    def backward(ctx, grad_y):
+        x2, weight, mean, rstd, normed, W1, W_down, preact = ctx.saved_tensors
+        need_b = ctx.needs_input_grad[2]
+        dy = grad_y.reshape(x2.shape).contiguous()
+        dn, dW1, dW_down = swiglu_mlp_bwd(normed, W1.contiguous(), W_down.contiguous(), preact, dy)
+        dbias = _bias_grad(x2, weight, ctx.bias_type) if need_b else None
+        dx, dw, db = swiglu_layer_norm_bwd(dn, x2, weight, mean, rstd, dres=dy, bias_grad=need_b, dbias=dbias)
+        return dx.reshape(grad_y.shape), dw if ctx.needs_input_grad[1] else None, db, dW1, dW_down, None
+
+
+def swiglu_prenorm_mlp(x, weight, bias, W1, W_down, eps=1e-5):
+    return SwiGLUPreNormMLPFunction.apply(x, weight, bias, W1, W_down, eps)

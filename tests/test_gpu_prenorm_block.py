@@ -1,0 +1,53 @@
+"""The block that the operators make with the MLP step: y = x + MLP(norm(x))
+against the definition in 64 bits, and the example that trains and serves it."""
+import os
+import sys
+
+import pytest
+import torch
+
+import bwd_gemm_epilogue_amd as sw
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+sys.path.insert(0, os.path.join(ROOT, "examples"))
+
+pytestmark = pytest.mark.gpu
+
+TOL = 1e-2  # of the largest value: bf16 storage of norm(x), preact, h and grad_preact, as the MLP step's own
+
+
+def close(got, ref):
+    ref = ref.double()
+    assert float((got.double().cpu() - ref).abs().max() / ref.abs().max()) <= TOL
+
+
+@pytest.mark.parametrize("M,D,I", [(1, 64, 64), (33, 128, 192), (300, 256, 512)])
+def test_block_and_gradients(M, D, I):
+    g = torch.Generator().manual_seed(M)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    bf = torch.bfloat16
+    x, W1, Wd, dy = r(M, D).to(bf), (r(D, 2 * I) * D ** -0.5).to(bf), (r(I, D) * I ** -0.5).to(bf), r(M, D).to(bf)
+    w, b = 1 + 0.2 * r(D), 0.2 * r(D)
+    leaves = [v.cuda().requires_grad_() for v in (x, w, b, W1, Wd)]
+    y = sw.swiglu_prenorm_mlp(*leaves)
+    y.backward(dy.cuda())
+    ref = [v.double().requires_grad_() for v in (x, w, b, W1, Wd)]
+    mu = ref[0].mean(1, keepdim=True)
+    n = (ref[0] - mu) / (((ref[0] - mu) ** 2).mean(1, keepdim=True) + 1e-5).sqrt() * ref[1] + ref[2]
+    pre = n @ ref[3]
+    want = ref[0] + (pre[:, :I] * torch.nn.functional.silu(pre[:, I:])) @ ref[4]
+    want.backward(dy.double())
+    close(y.detach(), want.detach())
+    for got, v in zip(leaves, ref):
+        assert got.grad.dtype == got.dtype
+        close(got.grad, v.grad)
+
+
+def test_example_trains_and_serves():
+    import prenorm_block
+    said = []
+    blocks, losses, norms = prenorm_block.train(D=128, I=256, tokens=512, layers=2, steps=12, say=said.append)
+    assert all(v == v and v < float("inf") for v in losses + norms)
+    assert losses[-1] < losses[0]
+    x, used = prenorm_block.serve([p.detach() for p in blocks[-1]], experts=6, k=2, tokens=3, steps=4, say=said.append)
+    assert x.shape == (3, 128) and bool(x.isfinite().all()) and int(used.sum()) == 3 * 2 * 4
