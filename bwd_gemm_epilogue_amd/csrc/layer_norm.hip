@@ -9,9 +9,13 @@
 // and, over all rows, dw = sum dy xh, db = sum dy.
 //
 // Both are bound by HBM: every element is read once into registers and written
-// once.  A row belongs to one wave (64 lanes) while a lane's share of it fits
-// its registers, so that the forward and the row part of the backward need
-// neither LDS nor a barrier; wider rows go to a workgroup.
+// once.  A row belongs to a wave where it is short, to a workgroup where it is
+// wide.  Measured at 11136 x 3584 bf16 with fp32 weights: the forward 24.2 us
+// (160 MB, 6.6 TB/s: the inputs come in part from the last-level cache, because
+// y is stored past it; with ordinary stores 39.7 us), the backward with the
+// residual branch's gradient 59.5 us (319 MB, 5.4 TB/s, what a copy of that size
+// reaches).  Small calls are bound by their launches: one row of 4096 takes 7 us
+// of the host, 2.5 of the GPU.
 #include "block_common.hpp"
 
 namespace swb {
@@ -451,9 +455,8 @@ __global__ void __launch_bounds__(256) ln_bwd_wide_cols_kernel(const BwdArgs a) 
 }
 
 // dw[c] (and db[c] = column D + c) = the parts' sum, in order.  A workgroup
-// takes 64 columns; its sixteen waves take a sixteenth of the parts each (at
-// 256 parts two rounds of eight loads; four waves with a quarter each took
-// 4.8 us instead of 3 at 7168 columns).
+// takes 64 columns; its sixteen waves take a sixteenth of the parts each: at 256
+// parts two rounds of eight loads.
 __global__ void __launch_bounds__(1024) ln_bwd_cols_kernel(const float* __restrict__ part, int parts, int D, int cols,
                                                            int wtype, void* dw, void* db) {
   __shared__ float red[16][64];
@@ -506,6 +509,9 @@ int fwd_go(const FwdArgs& a, hipStream_t st) {
   return launch_status();
 }
 
+// Threads to a row by its width (us): a wave with 8, 16 or 32 elements a lane up
+// to 2048 (11136 x 2048 bf16: 14.5; a workgroup: 16.5), a workgroup of 256 above
+// (11136 x 3584: 24.0; a wave with 64: 25.7; 32 elements to a thread: 29).
 template <class T, class W>
 int fwd_typed(const FwdArgs& a, hipStream_t st) {
   if (a.D <= 64 * 8) return fwd_go<T, W, 64, 8>(a, st);
@@ -518,24 +524,41 @@ int fwd_typed(const FwdArgs& a, hipStream_t st) {
   return launch_status();
 }
 
-// The row pass: G threads to a row, E elements of it to a thread.
+// Workgroups of the row pass, and so parts of dw and db: one for every compute
+// unit (512 take 63.1 us instead of 59.5 at 11136 x 3584, 128 take 115: the parts
+// are written and read again).  Where those would have one or two rounds and
+// half of them only one, half as many with two rounds each write half the
+// parts: 333 x 8191 fp32 12.9 against 13.9 us, 300 x 4096 bf16 10.2 against 11.4;
+// past one and a half rounds it does not pay (500 x 4096: 13.7 against 12.1).
+int64_t row_groups(int64_t blocks) {
+  if (blocks <= kBwdGroups) return blocks;
+  if (blocks <= kBwdGroups * 3 / 2) return ((blocks + 1) / 2 + 7) / 8 * 8;
+  return kBwdGroups;
+}
+
+// G threads to a row, E elements of it to a thread.
 template <class T, class W, int G, int E, int THREADS, bool AHEAD = true>
 int bwd_go(const BwdArgs& a, int64_t* parts, hipStream_t st) {
-  const int64_t blocks = (a.M + THREADS / G - 1) / (THREADS / G);
-  // as many workgroups as finish in the same number of rounds
-  const int64_t rounds = (blocks + kBwdGroups - 1) / kBwdGroups;
-  *parts = (blocks + rounds - 1) / rounds;
-  hipLaunchKernelGGL((ln_bwd_kernel<T, W, G, E / Vec<T>::N, THREADS, AHEAD>), dim3((unsigned)*parts), dim3(THREADS), 0, st, a);
+  *parts = row_groups((a.M + THREADS / G - 1) / (THREADS / G));
+  hipLaunchKernelGGL((ln_bwd_kernel<T, W, G, E / Vec<T>::N, THREADS, AHEAD>), dim3((unsigned)*parts), dim3(THREADS), 0,
+                     st, a);
   return launch_status();
 }
 
+// Threads to a row by its width, each side measured at two widths or more
+// (bf16, us): up to 512 a wave with 8 elements a lane (11136 x 512: 14.9; with
+// 16: 15.4), up to 1024 a wave with 16 (16384 x 1024: 30.4; a workgroup of 512
+// threads for two rows: 37), to 2048 two rows of 256 threads (11136 x 2048:
+// 38.4; a wave with 32: 40.9), to 4096 256 threads with 16 (11136 x 3584: 62.6;
+// two rows 65.6, 32 elements 68.4), to 8192 512 threads with 16 (1000 x 6000:
+// 15.2; 256 with 32: 17.2).
 template <class T, class W>
 int bwd_typed(const BwdArgs& a, int64_t* parts, hipStream_t st) {
   if (a.D <= 64 * 8) return bwd_go<T, W, 64, 8, 512>(a, parts, st);
   if (a.D <= 64 * 16) return bwd_go<T, W, 64, 16, 256>(a, parts, st);
   if (a.D <= 256 * 8) return bwd_go<T, W, 256, 8, 512>(a, parts, st);
   if (a.D <= 256 * 16) return bwd_go<T, W, 256, 16, 256>(a, parts, st);
-  if (a.D <= 256 * 32) return bwd_go<T, W, 256, 32, 256>(a, parts, st);
+  if (a.D <= 512 * 16) return bwd_go<T, W, 512, 16, 512>(a, parts, st);
   if (a.D <= 512 * 32) return bwd_go<T, W, 512, 32, 512, false>(a, parts, st);
   *parts = a.M < kBwdGroups ? a.M : kBwdGroups;
   hipLaunchKernelGGL((ln_bwd_wide_kernel<T, W>), dim3((unsigned)a.M), dim3(256), 0, st, a);
