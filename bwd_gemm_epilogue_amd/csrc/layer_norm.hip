@@ -51,14 +51,17 @@ struct FwdArgs {
   double eps;
 };
 
-// 1 / sqrt(v): the hardware's reciprocal square root, one Newton step to round
-// it as well as a division would
+// 1 / sqrt(var + eps): the hardware's reciprocal square root and one Newton step.
+// Below 2^-100 (eps = 0 and a row of very small spread) the argument is scaled out
+// of the range that the instruction may take for zero.
 __device__ __forceinline__ float rstd_of(float var, float eps) {
-  const float a = var + eps;
+  const float v = var + eps;
+  const bool tiny = v < 0x1p-100f;
+  const float a = tiny ? v * 0x1p+60f : v;
   float r = __builtin_amdgcn_rsqf(a);
-  const float e = __builtin_fmaf(-a * r, r, 1.0f);
   // a = 0 or inf: r is inf or 0 and stays
-  return (a > 0.0f && a < __builtin_inff()) ? __builtin_fmaf(0.5f * r, e, r) : r;
+  if (a > 0.0f && a < __builtin_inff()) r = __builtin_fmaf(0.5f * r, __builtin_fmaf(-a * r, r, 1.0f), r);
+  return tiny ? r * 0x1p+30f : r;
 }
 
 // One row to G threads, NV 16-byte vectors of it to a thread, and the D % VEC
@@ -500,6 +503,7 @@ namespace {
 using namespace swb;
 
 constexpr int64_t kMaxNormDim = (int64_t)1 << 20;
+constexpr int64_t kLaunchRows = (int64_t)1 << 23;
 constexpr int64_t kBwdGroups = 256;  // workgroups of the row pass at most, and parts of dw and db
 
 template <class T, class W, int G, int E>
@@ -561,6 +565,7 @@ int bwd_typed(const BwdArgs& a, int64_t* parts, hipStream_t st) {
   if (a.D <= 512 * 16) return bwd_go<T, W, 512, 16, 512>(a, parts, st);
   if (a.D <= 512 * 32) return bwd_go<T, W, 512, 32, 512, false>(a, parts, st);
   *parts = a.M < kBwdGroups ? a.M : kBwdGroups;
+  // M * 16385 elements at least: far fewer than 2^24 rows fit the memory
   hipLaunchKernelGGL((ln_bwd_wide_kernel<T, W>), dim3((unsigned)a.M), dim3(256), 0, st, a);
   SW_TRY(launch_status());
   if (!a.part) return SWIGLU_OK;
@@ -628,8 +633,24 @@ int swiglu_layer_norm_fwd(const void* x, int64_t ldx, const void* weight, const 
   const Range outs[] = {rows_range(y, M, ldy, D, es), rng(mean, M * 4), rng(rstd, M * 4)};
   SW_TRY(check_alias(ins, 3, outs, 3));
   if (M == 0) return SWIGLU_OK;
-  const FwdArgs a{x, weight, bias, y, mean, rstd, ldx, ldy, M, (int)D, (float)(1.0 / (double)D), eps};
-  return by_type(dtype, wdtype, [&](auto t, auto w) { return fwd_typed<decltype(t), decltype(w)>(a, as_stream(stream)); });
+  // a launch holds fewer than 2^32 threads: at most kLaunchRows workgroups of 256
+  for (int64_t r = 0; r < M; r += kLaunchRows) {
+    const FwdArgs a{(const char*)x + r * ldx * es,
+                    weight,
+                    bias,
+                    (char*)y + r * ldy * es,
+                    mean ? mean + r : nullptr,
+                    rstd ? rstd + r : nullptr,
+                    ldx,
+                    ldy,
+                    M - r < kLaunchRows ? M - r : kLaunchRows,
+                    (int)D,
+                    (float)(1.0 / (double)D),
+                    eps};
+    SW_TRY(by_type(dtype, wdtype,
+                   [&](auto t, auto w) { return fwd_typed<decltype(t), decltype(w)>(a, as_stream(stream)); }));
+  }
+  return SWIGLU_OK;
 }
 
 size_t swiglu_layer_norm_bwd_workspace(int64_t M, int64_t D) {

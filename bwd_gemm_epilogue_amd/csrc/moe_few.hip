@@ -287,7 +287,7 @@ constexpr int kRouteInline = 256;  // logits (tokens times experts)
 constexpr int kPartRows = 16, kPartValues = 8192;  // rows and values of h that a kDownPart workgroup makes
 
 template <int NT, int WAVES, Kind KIND, bool FEW, int AHEAD>
-__global__ void __launch_bounds__(WAVES * 64, AHEAD > 2 ? 1 : NT == 1 ? 4 : 2) few_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(WAVES * 64, AHEAD > 2 ? 1 : NT > 1 ? 2 : KIND < kDown ? 4 : 3) few_kernel(const FewArgs a) {
   constexpr bool GATE = KIND == kGate || KIND == kGateRoute;
   constexpr int THREADS = WAVES * 64;
   __shared__ Rows sh;

@@ -206,6 +206,32 @@ def test_constant_rows_infinities_and_nan_stay_in_their_rows():
     assert dx.cpu()[[0, 1, 2, 5]].isfinite().all() and dx.cpu()[[3, 4]].isnan().all()
 
 
+def test_more_rows_than_one_launch():
+    """2^24 + 3 rows of one element: the element is its own mean and y the bias."""
+    M = (1 << 24) + 3
+    x = (torch.arange(M, device="cuda") % 251).to(torch.bfloat16).reshape(M, 1)
+    w, b = torch.full((1,), 2.0, device="cuda"), torch.full((1,), 0.75, device="cuda")
+    y, mean, rstd = sw.swiglu_layer_norm_fwd(x, w, b, EPS)
+    assert (y == 0.75).all() and torch.equal(mean, x[:, 0].float())
+    assert ((rstd - EPS ** -0.5).abs() <= 4 * E32 * EPS ** -0.5).all()
+
+
+def test_small_spreads_without_epsilon():
+    """eps = 0 and rows scaled by powers of two down to where the second moment
+    leaves fp32's normals: rstd scales by the inverse, exactly while it is normal."""
+    x = torch.randn(1, 500, generator=torch.Generator().manual_seed(2)).repeat(5, 1)
+    s = torch.tensor([0, -30, -50, -55, -62])
+    x = x * torch.exp2(s.double())[:, None].float()
+    y, mean, rstd = sw.swiglu_layer_norm_fwd(x.cuda(), eps=0.0)
+    r = rstd.cpu().double() * torch.exp2(s.double())
+    # the same roundings, but the root's in the scaled range; at 2^-124 a square may
+    # be below the normals and is off by 2^-150, a quarter of e of the mean square
+    assert ((r - r[0]).abs() <= 8 * E32 * r[0]).all()
+    assert y.isfinite().all()
+    z = sw.swiglu_layer_norm_fwd(torch.ones(2, 300, device="cuda"), eps=0.0)
+    assert z[2].isinf().all() and z[0].isnan().all()      # no spread at all: 0 * inf
+
+
 def test_no_rows():
     x = torch.empty(0, 96, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(96, device="cuda")
