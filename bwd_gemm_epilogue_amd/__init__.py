@@ -2,7 +2,8 @@
 
 Every function here only marshals arguments (torch tensors -> device
 pointers, the current HIP stream) and calls the C ABI declared in
-``include/swiglu_mlp.h``; all arithmetic runs in the HIP kernels.  There is
+``include/swiglu_mlp.h`` (the step) and ``include/swiglu_block.h`` (the
+operators around it, in ``block.py``); all arithmetic runs in the HIP kernels.  There is
 no CPU fallback: importing fails loudly when the library is not built, and
 calls fail loudly on tensors that are not bf16 on a GPU.
 
@@ -181,20 +182,22 @@ def _stream(t: torch.Tensor, stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-# The handle of the current stream without a stream object around it (0.1 us
-# against 2.7 us of a call's host time).
+# The current device, and the handle of its stream without a stream object
+# around it (0.1 us against 2.7 us of a call's host time).  Asked only once a
+# tensor on a GPU is there, so the runtime is up.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _launches(fn):
-    """Run a launching call with its first tensor's device (or that of the
-    first tensor of its first list) current and the launch stream as torch's current stream.  Every tensor the call
-    allocates (outputs, a temporary workspace) then belongs to that stream in
-    the caching allocator, so a temporary freed on return is not handed to
-    other work before the launched kernels are done with it.  `stream` may
-    be a torch stream or a raw HIP stream handle (wrapped as an external
-    stream)."""
+    """Run a launching call with its first tensor's device current and the
+    launch stream as torch's current stream (of a first argument that is a list,
+    the first tensor counts).  Every tensor the call allocates (outputs, a
+    temporary workspace) then belongs to that stream in the caching allocator, so
+    a temporary freed on return is not handed to other work before the launched
+    kernels are done with it.  `stream` may be a torch stream or a raw HIP stream
+    handle (wrapped as an external stream)."""
     params = list(inspect.signature(fn).parameters)
     at = params.index("stream")
 
@@ -204,15 +207,17 @@ def _launches(fn):
             kw["stream"] = args[at]
             args = args[:at]
         like = args[0] if args else None
-        if isinstance(like, (list, tuple)):
+        if not isinstance(like, torch.Tensor) and isinstance(like, (list, tuple)):
             like = next((t for t in like if t is not None), None)
         if not isinstance(like, torch.Tensor) or not like.is_cuda:
             raise ValueError(f"{fn.__name__}: the first argument must be a tensor on a GPU (no CPU path)")
         stream = kw.get("stream")
-        if stream is None and like.get_device() == torch.cuda.current_device():
-            # the device and its stream are current already: the handle alone
-            kw["stream"] = _raw_stream(like.get_device())
-            return fn(*args, **kw)
+        if stream is None:
+            device = like.get_device()
+            if device == _current_device():
+                # the device and its stream are current already: the handle alone
+                kw["stream"] = _raw_stream(device)
+                return fn(*args, **kw)
         if stream is None:
             st = torch.cuda.current_stream(like.device)
         elif isinstance(stream, torch.cuda.Stream):

@@ -243,7 +243,9 @@ __global__ void __launch_bounds__(THREADS) ln_bwd_kernel(const BwdArgs a) {
     for (int i = 0; i < NV; ++i) {
       const int v = tl + i * G;
       if (v < nvec) {
-        q.x[i] = load_vec(x + v * VEC);
+        // x was read long ago and is not read again: past the caches, which may
+        // hold dy and the residual's gradient (4096 x 4096: 29.3 -> 26.6 us)
+        q.x[i] = last_vec(x + v * VEC);
         q.y[i] = load_vec(dy + v * VEC);
         if (AHEAD && a.dres) q.r[i] = load_vec(rs + v * VEC);
       }
