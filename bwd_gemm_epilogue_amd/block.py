@@ -13,6 +13,7 @@ import ctypes
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (SwiGLUError, _check, _launches, _on_gpu, _stream, _ws, lib, swiglu_fwd_down_residual, swiglu_fwd_gemm1,
                swiglu_mlp_bwd)
@@ -207,6 +208,7 @@ class SwiGLULayerNormFunction(torch.autograd.Function):
         return y.reshape(x.shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_y):
         x2, weight, mean, rstd = ctx.saved_tensors
         _, need_w, need_b, _ = ctx.needs_input_grad
@@ -411,6 +413,7 @@ class SwiGLUPreNormMLPFunction(torch.autograd.Function):
         return y.reshape(x.shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_y):
         x2, weight, mean, rstd, normed, W1, W_down, preact = ctx.saved_tensors
         need_b = ctx.needs_input_grad[2]

@@ -13,7 +13,7 @@
 // wide.  Measured at 11136 x 3584 bf16 with fp32 weights: the forward 24.2 us
 // (160 MB, 6.6 TB/s: the inputs come in part from the last-level cache, because
 // y is stored past it; with ordinary stores 39.7 us), the backward with the
-// residual branch's gradient 59.5 us (319 MB, 5.4 TB/s, what a copy of that size
+// residual branch's gradient 58.7 us (319 MB, 5.4 TB/s, what a copy of that size
 // reaches).  Small calls are bound by their launches: one row of 4096 takes 7 us
 // of the host, 2.5 of the GPU.
 #include "block_common.hpp"

@@ -44,9 +44,9 @@ constexpr int kRouteSlice = kRouteWaves * 64;  // rows of Wr of one workgroup, 6
 // One workgroup: 16 tokens, 16 experts, 256 d; a wave has 64 of them, in sixteen
 // v_mfma_f64_16x16x4.  Lane 16 g + j holds token j's and expert j's values at d =
 // 8 g + i (and 32 + 8 g + i) in step i, so a token's eight are one load.
-__global__ void __launch_bounds__(kRouteWaves * 64) route_logits_kernel(const uint16_t* __restrict__ x,
-                                                           const uint16_t* __restrict__ wr, double* __restrict__ part,
-                                                           int M, int D, int E) {
+__global__ void __launch_bounds__(kRouteWaves * 64)
+    route_logits_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr, double* __restrict__ part,
+                        int M, int D, int E) {
   __shared__ f64x4 sums[kRouteWaves - 1][64];
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -241,6 +241,15 @@ __device__ __forceinline__ bool find_expert(const FewArgs& a, const int* ids, in
   return true;
 }
 
+// h in two bf16 halves whose sum carries 16 bits.  An infinite h (or one that
+// rounds to it) has no lower half: inf - inf would make it a NaN.
+__device__ __forceinline__ void halves(float h, uint16_t& hi, uint16_t& lo) {
+  const bf16_t top = (bf16_t)h;
+  const float rest = h - (float)top;
+  hi = __builtin_bit_cast(uint16_t, top);
+  lo = __builtin_bit_cast(uint16_t, (bf16_t)(__builtin_fabsf((float)top) < __builtin_inff() ? rest : 0.0f));
+}
+
 // Loads of the main loop are buffer loads: a scalar descriptor, a lane offset
 // held for the whole loop and a scalar offset.  (As global loads the compiler
 // kept a 64-bit address in registers for each of a step's rows, which spilled.)
@@ -253,25 +262,6 @@ __device__ __forceinline__ u32x4 load16(brsrc_t r, uint32_t lane_at, uint32_t at
   return __builtin_amdgcn_raw_buffer_load_b128(r, (int)lane_at, (int)at, STREAM ? 2 : 0);
 }
 
-// One workgroup: up to 16 * NT rows of one expert times 128 columns of its
-// matrix over one part of K.
-//
-// The weights go from memory to the matrix cores through registers only.  A wave
-// step covers 32 rows of W: lane l loads 16 bytes (8 columns, chunk l % 16) of
-// each of the rows 8 (l / 16) + 0..7, and so holds, for each of its 8 columns,
-// the eight consecutive k that v_mfma_f32_16x16x32_bf16 wants of column l % 16
-// in one lane; a byte permute for each pair of rows puts them together (32 for
-// the 8 KB of a step).  Product c of the 8 then covers columns 8 j + c, j = 0..15.
-// No LDS, no barrier, and two steps of loads in flight in each wave; the waves
-// take every WAVES-th step and their sums meet in LDS at the end.
-//
-// Gate/up: W1, columns 64 b .. + 63 of the left half beside those of the gate half
-// (chunks 8..15).  Without a split of K the workgroup has all of left and gate of
-// its channels and writes h itself, in two bf16 halves whose sum carries 16 bits
-// (the second product of the down matrix costs no time: HBM bounds it).
-// Four waves: with eight 32 tokens take 134 us instead of 132, 64 tokens over 64
-// experts 129 instead of 108 (fewer workgroups on a compute unit, whose starts
-// and ends the others' loads have to hide).
 template <int V>
 struct int_c {
   static constexpr int value = V;
@@ -283,11 +273,40 @@ enum Kind {
   kDown,       // from h
   kDownPart    // from the gate/up's parts
 };
-constexpr int kRouteInline = 256;  // logits (tokens times experts)
-constexpr int kPartRows = 16, kPartValues = 8192;  // rows and values of h that a kDownPart workgroup makes
+// Logits (tokens times experts) that every workgroup of the gate/up launch ranks
+// for itself, which saves a launch: one token over 16 experts 31.8 -> 29.9 us.
+// More cost more than the launch: 7 tokens over 60 experts 81.6 against 87.4.
+constexpr int kRouteInline = 256;
+// Rows and values of h that a kDownPart workgroup makes (33 KB of LDS).
+constexpr int kPartRows = 16, kPartValues = 8192;
 
+// One workgroup: the rows of one expert, 16 T at a time, times 128 columns of its
+// matrix over one part of K.
+//
+// The weights go from memory to the matrix cores through registers only.  A wave
+// step covers 32 rows of W: lane l loads 16 bytes (8 columns, chunk l % 16) of
+// each of the rows 8 (l / 16) + 0..7, and so holds, for each of its 8 columns,
+// the eight consecutive k that v_mfma_f32_16x16x32_bf16 wants of column l % 16
+// in one lane; a byte permute for each pair of rows puts them together (32 for
+// the 8 KB of a step).  Product c of the 8 then covers columns 8 j + c, j = 0..15.
+// The main loop has no barrier and AHEAD steps of loads in flight in each wave;
+// the waves take every WAVES-th step and their sums meet in LDS at the end.
+//
+// Gate/up: W1, columns 64 b .. + 63 of the left half beside those of the gate half
+// (chunks 8..15).  Without a split of K the workgroup has all of left and gate of
+// its channels and writes h itself, in two halves (the second product of the down
+// matrix costs no time: HBM bounds it).
+//
+// What bounds it: HBM.  32 tokens over 16 experts of 3584 x 2048: gate/up 470 MB
+// in 84 us, down 235 MB in 41 us, 5.6 TB/s.  One token: 13 and 7 us for 59 and 29
+// MB, of which about 3 us each are start (the ids, the first loads) and end.
+// Four waves: with eight 32 tokens take 134 us instead of 132, 64 tokens over 64
+// experts 129 instead of 108 (fewer workgroups on a compute unit, whose starts
+// and ends the others' loads have to hide).  Ordinary instead of streaming loads:
+// 145 against 134 us at 32 tokens.
 template <int NT, int WAVES, Kind KIND, bool FEW, int AHEAD>
-__global__ void __launch_bounds__(WAVES * 64, AHEAD > 2 ? 1 : NT > 1 ? 2 : KIND < kDown ? 4 : 3) few_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(WAVES * 64, AHEAD > 2 ? 1 : NT > 1 ? 2 : KIND < kDown ? 4 : 3)
+    few_kernel(const FewArgs a) {
   constexpr bool GATE = KIND == kGate || KIND == kGateRoute;
   constexpr int THREADS = WAVES * 64;
   __shared__ Rows sh;
@@ -359,12 +378,7 @@ __global__ void __launch_bounds__(WAVES * 64, AHEAD > 2 ? 1 : NT > 1 ? 2 : KIND 
       }
       uint16_t hi[4], lo[4];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const float hv = swg::swiglu_h(left[v], gate[v]);
-        const bf16_t t = (bf16_t)hv;
-        hi[v] = __builtin_bit_cast(uint16_t, t);
-        lo[v] = __builtin_bit_cast(uint16_t, (bf16_t)(hv - (float)t));
-      }
+      for (int v = 0; v < 4; ++v) halves(swg::swiglu_h(left[v], gate[v]), hi[v], lo[v]);
       uint16_t* o = hs + r * hpitch + c;
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
@@ -484,11 +498,7 @@ __global__ void __launch_bounds__(WAVES * 64, AHEAD > 2 ? 1 : NT > 1 ? 2 : KIND 
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             const float gate = __shfl_down(v[c], 8, 64);
-            const float hv = swg::swiglu_h(v[c], gate);
-            const bf16_t top = (bf16_t)hv;
-            const bf16_t low = (bf16_t)(hv - (float)top);
-            hi[c] = __builtin_bit_cast(uint16_t, top);
-            lo[c] = __builtin_bit_cast(uint16_t, low);
+            halves(swg::swiglu_h(v[c], gate), hi[c], lo[c]);
           }
           if (live && q < 8) {
             uint16_t* hp = a.h + (int64_t)p * I + blockIdx.x * 64 + q * 8;
@@ -570,7 +580,9 @@ constexpr int kWaves = 4;
 int64_t route_slices(int64_t D) { return (D + kRouteSlice - 1) / kRouteSlice; }
 
 // Parts of K: so many that the launch has a workgroup for every compute unit
-// when every slot has its expert, but at least a step of 32 for every wave.
+// when every slot has its expert, but at least a step of 32 for every wave.  One
+// token, two experts: four parts 29.7 us, one 45.5; two workgroups for every
+// unit 34.1 (more parts to write and read).
 int few_splits(int64_t blocks, int64_t slots, int64_t K) {
   int64_t s = kUnits / (blocks * slots);
   const int64_t most = K / (32 * kWaves);
@@ -628,7 +640,8 @@ size_t route_bytes(int64_t M, int64_t D, int64_t E) { return align256((size_t)(r
 int run_logits(const void* x, const void* wr, void* part, int64_t M, int64_t D, int64_t E, hipStream_t st) {
   hipLaunchKernelGGL(route_logits_kernel,
                      dim3((unsigned)route_slices(D), (unsigned)((M + 15) / 16), (unsigned)((E + 15) / 16)),
-                     dim3(kRouteWaves * 64), 0, st, (const uint16_t*)x, (const uint16_t*)wr, (double*)part, (int)M, (int)D, (int)E);
+                     dim3(kRouteWaves * 64), 0, st, (const uint16_t*)x, (const uint16_t*)wr, (double*)part, (int)M, (int)D,
+                     (int)E);
   return launch_status();
 }
 int run_topk(const void* part, int* ids, float* weights, int64_t M, int64_t D, int64_t E, int64_t k, int renorm,

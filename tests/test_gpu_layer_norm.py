@@ -278,6 +278,13 @@ def test_autograd_of_views_and_expanded_gradients():
     assert float(x.grad.float().abs().max()) <= 100 * E32 * 50
 
 
+def test_a_second_derivative_is_refused():
+    x = torch.randn(3, 20, device="cuda", requires_grad=True)
+    g, = torch.autograd.grad(sw.swiglu_layer_norm(x).square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
+
+
 def test_same_bits_every_time_and_on_another_stream():
     x, w, b, dy, res = make(1500, 1111, torch.bfloat16, torch.float32)
     X, W, B, DY, R = cuda(x, w, b, dy, res)

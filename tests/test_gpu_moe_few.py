@@ -152,6 +152,23 @@ def test_infinite_and_nan_tokens_stay_theirs():
     assert w[1].isnan().all() and w[4].isnan().all() and y[1].isnan().all() and y[4].isnan().all()
 
 
+@pytest.mark.parametrize("tokens", [1, 20])
+def test_h_past_32_bits_stays_infinite(tokens):
+    """A pre-activation that overflows: h is infinite, not NaN, and so is y where
+    its weight is not zero (20 tokens: h goes through memory, one: through the
+    down launch)."""
+    D, I, N = 512, 64, 64
+    x = torch.zeros(tokens, D, dtype=torch.bfloat16)
+    x[:, 0], x[:, 1] = 3e38, 1.0
+    W1, Wd = torch.zeros(2, D, 2 * I, dtype=torch.bfloat16), torch.zeros(2, I, N, dtype=torch.bfloat16)
+    W1[:, 0, 5], W1[:, 1, I + 5] = 2.0, 1.0            # left 6e38, gate 1
+    Wd[:, 5, 0], Wd[:, 5, 1], Wd[:, 7, 2] = 1.0, -1.0, 1.0
+    ids = (torch.arange(tokens, dtype=torch.int32) % 2).reshape(tokens, 1)
+    y = sw.swiglu_moe_few_fwd(x.cuda(), W1.cuda(), Wd.cuda(), ids.cuda(), torch.ones(tokens, 1, device="cuda")).cpu()
+    assert (y[:, 0] == float("inf")).all() and (y[:, 1] == -float("inf")).all()
+    assert y[:, 2:].isnan().all()                      # inf * 0
+
+
 def test_large_logits_and_minus_infinity():
     x = torch.zeros(2, 64, dtype=torch.bfloat16)
     x[:, 0] = 1.0
