@@ -3,10 +3,12 @@ in a block that trains or serves it.  As in the rest of the package every
 function marshals arguments only; the arithmetic runs in the HIP kernels and
 there is no CPU path.
 
-The regular case of each short call goes through the native half of the
-binding (csrc/host.cpp), which checks, allocates and launches at a fraction of
-the cost; what it does not take comes back as None and is done, or refused,
-here."""
+The regular case of each short call (on the current device and stream, outputs
+to be allocated) goes through the native half of the binding (csrc/host.cpp),
+which checks, allocates and launches at a fraction of the cost; what it does not
+take comes back as None and is done, or refused, by the function's general form
+(its __wrapped__), which runs inside a launch context like the package's other
+calls and words what is missing: the fronts' last operands default to None."""
 from __future__ import annotations
 
 import ctypes
@@ -104,14 +106,7 @@ def _norm_type(x, v):
 
 
 @_launches
-def swiglu_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=None, stream=None):
-    """y = (x - mean) rstd weight + bias over the last dimension of x [M,D]
-    (dense rows, any row stride): returns (y, mean, rstd), the statistics
-    float32 [M]."""
-    if y is None and mean is None and rstd is None:
-        got = _host().layer_norm_fwd(x, weight, bias, eps, _stream(x, stream))
-        if got is not None:
-            return _native("swiglu_layer_norm_fwd", got)
+def _layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=None, stream=None):
     if x.dim() != 2:
         raise ValueError(f"x must have two dimensions, got {tuple(x.shape)}")
     shape, t, dev = x.shape, x.dtype, x.get_device()
@@ -134,21 +129,27 @@ def swiglu_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None
     return y, mean, rstd
 
 
+def swiglu_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=None, stream=None):
+    """y = (x - mean) rstd weight + bias over the last dimension of x [M,D]
+    (dense rows, any row stride): returns (y, mean, rstd), the statistics
+    float32 [M]."""
+    if stream is None and y is None and mean is None and rstd is None:
+        got = _host().layer_norm_fwd(x, weight, bias, eps, None)
+        if got is not None:
+            return _native("swiglu_layer_norm_fwd", got)
+    return _layer_norm_fwd(x, weight, bias, eps, y, mean, rstd, stream)
+
+
+swiglu_layer_norm_fwd.__wrapped__ = _layer_norm_fwd
+
+
 def swiglu_layer_norm_bwd_workspace(M, D) -> int:
     return lib().swiglu_layer_norm_bwd_workspace(M, D)
 
 
 @_launches
-def swiglu_layer_norm_bwd(dy, x, weight, mean, rstd, dres=None, bias_grad=True, dx=None, dweight=None, dbias=None,
-                          ws=None, stream=None):
-    """Backward of swiglu_layer_norm_fwd: (dx, dweight, dbias).  dres [M,D] is
-    added to dx (the gradient that reaches x by a residual branch).  dweight
-    is None where weight is; dbias is None unless bias_grad (its type is the
-    weight's, or x's where there is none)."""
-    if dx is None and dweight is None and dbias is None and ws is None:
-        got = _host().layer_norm_bwd(dy, x, weight, mean, rstd, dres, bias_grad, _stream(x, stream))
-        if got is not None:
-            return _native("swiglu_layer_norm_bwd", got)
+def _layer_norm_bwd(dy, x, weight, mean, rstd=None, dres=None, bias_grad=True, dx=None, dweight=None, dbias=None, ws=None,
+                    stream=None):
     if x.dim() != 2:
         raise ValueError(f"x must have two dimensions, got {tuple(x.shape)}")
     shape, t, dev = x.shape, x.dtype, x.get_device()
@@ -178,6 +179,22 @@ def swiglu_layer_norm_bwd(dy, x, weight, mean, rstd, dres=None, bias_grad=True, 
         rp, ldr, dxp, lddx, dwp, dbp, ws.data_ptr(), ws.numel() * ws.element_size(), M, D, code, _DTYPES[wt],
         _stream(x, stream)))
     return dx, dweight, dbias
+
+
+def swiglu_layer_norm_bwd(dy, x, weight, mean, rstd=None, dres=None, bias_grad=True, dx=None, dweight=None, dbias=None,
+                          ws=None, stream=None):
+    """Backward of swiglu_layer_norm_fwd: (dx, dweight, dbias).  dres [M,D] is
+    added to dx (the gradient that reaches x by a residual branch).  dweight
+    is None where weight is; dbias is None unless bias_grad (its type is the
+    weight's, or x's where there is none)."""
+    if stream is None and dx is None and dweight is None and dbias is None and ws is None:
+        got = _host().layer_norm_bwd(dy, x, weight, mean, rstd, dres, bias_grad, None)
+        if got is not None:
+            return _native("swiglu_layer_norm_bwd", got)
+    return _layer_norm_bwd(dy, x, weight, mean, rstd, dres, bias_grad, dx, dweight, dbias, ws, stream)
+
+
+swiglu_layer_norm_bwd.__wrapped__ = _layer_norm_bwd
 
 
 def _as_rows(t: torch.Tensor) -> torch.Tensor:
@@ -245,11 +262,8 @@ def _addresses(tensors, name: str, dev: int):
     return [t.data_ptr() for t in tensors], codes
 
 
-def _clip(grads, max_norm, outs, total, ws, stream):
-    if total is None and ws is None and not isinstance(grads, torch.Tensor):
-        got = _host().clip_grad_norm(grads, outs, float(max_norm), _stream(None, stream))
-        if got is not None:
-            return _native("swiglu_clip_grad_norm", got)
+@_launches
+def _clip_grad_norm(grads, max_norm, outs=None, total=None, ws=None, stream=None):
     if isinstance(grads, torch.Tensor):
         grads, outs = [grads], None if outs is None else [outs]
     if outs is not None and len(outs) != len(grads):
@@ -276,20 +290,25 @@ def _clip(grads, max_norm, outs, total, ws, stream):
     return total
 
 
-@_launches
 def swiglu_clip_grad_norm(grads, max_norm, outs=None, total=None, ws=None, stream=None):
     """Scale the gradients (a list of contiguous tensors of any sizes and of
     bfloat16, float16 or float32; None entries are passed over) by min(1,
     max_norm / (total + 1e-6)), total the 2-norm of all of them together, in
     place or into `outs`.  Returns total, a float32 scalar on the GPU: the
     host does not wait."""
-    return _clip(grads, max_norm, outs, total, ws, stream)
+    if stream is None and total is None and ws is None:
+        got = _host().clip_grad_norm(grads, outs, float(max_norm), None)
+        if got is not None:
+            return _native("swiglu_clip_grad_norm", got)
+    return _clip_grad_norm(grads, max_norm, outs, total, ws, stream)
 
 
-@_launches
 def swiglu_grad_norm(grads, total=None, ws=None, stream=None):
     """The 2-norm of all gradients together, a float32 scalar on the GPU."""
-    return _clip(grads, math.inf, None, total, ws, stream)
+    return swiglu_clip_grad_norm(grads, math.inf, total=total, ws=ws, stream=stream)
+
+
+swiglu_clip_grad_norm.__wrapped__ = swiglu_grad_norm.__wrapped__ = _clip_grad_norm
 
 
 # --------------------------------------------------------------------------
@@ -345,14 +364,7 @@ def _experts(x, W1, W_down, dev):
 
 
 @_launches
-def swiglu_moe_few_fwd(x, W1, W_down, ids, weights, y=None, ws=None, stream=None):
-    """y[m] = sum_j weights[m,j] MLP_{ids[m,j]}(x[m]) for up to 64 tokens: x
-    [M,D], W1 [E,D,2I], W_down [E,I,Dout], ids int32 [M,k], weights float32
-    [M,k].  An id outside [0, E) adds nothing."""
-    if y is None and ws is None:
-        got = _host().moe_few(x, None, W1, W_down, ids, weights, _stream(x, stream))
-        if got is not None:
-            return _native("swiglu_moe_few_fwd", got)
+def _moe_few_fwd(x, W1, W_down, ids, weights=None, y=None, ws=None, stream=None):
     dev = x.get_device()
     xp = _typed(x, "x", x.shape, _BF16, dev)
     M, D, I, Dout, E, w1p, wdp = _experts(x, W1, W_down, dev)
@@ -366,19 +378,29 @@ def swiglu_moe_few_fwd(x, W1, W_down, ids, weights, y=None, ws=None, stream=None
     return y
 
 
-@_launches
-def swiglu_moe_few_layer(x, W_router, W1, W_down, k, renormalize=True, y=None, ids=None, weights=None, ws=None,
-                         stream=None):
-    """The whole layer for up to 64 tokens, router and experts: (y [M,Dout],
-    ids int32 [M,k], weights float32 [M,k])."""
-    if y is None and ids is None and weights is None and ws is None:
-        got = _host().moe_few(x, W_router, W1, W_down, k, bool(renormalize), _stream(x, stream))
+def swiglu_moe_few_fwd(x, W1, W_down, ids, weights=None, y=None, ws=None, stream=None):
+    """y[m] = sum_j weights[m,j] MLP_{ids[m,j]}(x[m]) for up to 64 tokens: x
+    [M,D], W1 [E,D,2I], W_down [E,I,Dout], ids int32 [M,k], weights float32
+    [M,k].  An id outside [0, E) adds nothing."""
+    if stream is None and y is None and ws is None:
+        got = _host().moe_few(x, None, W1, W_down, ids, weights, None)
         if got is not None:
-            return _native("swiglu_moe_few_layer", got)
+            return _native("swiglu_moe_few_fwd", got)
+    return _moe_few_fwd(x, W1, W_down, ids, weights, y, ws, stream)
+
+
+swiglu_moe_few_fwd.__wrapped__ = _moe_few_fwd
+
+
+@_launches
+def _moe_few_layer(x, W_router, W1, W_down, k=None, renormalize=True, y=None, ids=None, weights=None, ws=None,
+                   stream=None):
     dev = x.get_device()
     xp = _typed(x, "x", x.shape, _BF16, dev)
     M, D, I, Dout, E, w1p, wdp = _experts(x, W1, W_down, dev)
     wrp = _typed(W_router, "W_router", (D, E), _BF16, dev)
+    if k is None:
+        raise TypeError("k, the number of experts to a token, is missing")
     y = x.new_empty((M, Dout)) if y is None else y
     ids = x.new_empty((M, k), dtype=torch.int32) if ids is None else ids
     weights = x.new_empty((M, k), dtype=_F32) if weights is None else weights
@@ -388,6 +410,20 @@ def swiglu_moe_few_layer(x, W_router, W1, W_down, k, renormalize=True, y=None, i
         _typed(weights, "weights", (M, k), _F32, dev), ws.data_ptr(), ws.numel() * ws.element_size(),
         M, D, I, Dout, E, k, bool(renormalize), _stream(x, stream)))
     return y, ids, weights
+
+
+def swiglu_moe_few_layer(x, W_router, W1, W_down, k=None, renormalize=True, y=None, ids=None, weights=None, ws=None,
+                         stream=None):
+    """The whole layer for up to 64 tokens, router and experts: (y [M,Dout],
+    ids int32 [M,k], weights float32 [M,k])."""
+    if stream is None and y is None and ids is None and weights is None and ws is None:
+        got = _host().moe_few(x, W_router, W1, W_down, k, bool(renormalize), None)
+        if got is not None:
+            return _native("swiglu_moe_few_layer", got)
+    return _moe_few_layer(x, W_router, W1, W_down, k, renormalize, y, ids, weights, ws, stream)
+
+
+swiglu_moe_few_layer.__wrapped__ = _moe_few_layer
 
 
 # --------------------------------------------------------------------------

@@ -4,7 +4,7 @@
 //
 // Every function here takes the regular case of its namesake in block.py:
 // tensors of the right types, shapes and layout on one GPU, outputs to be
-// allocated.  It returns the result, or the negative status of a call that
+// allocated, and, where the stream is None, on the current device.  It returns the result, or the negative status of a call that
 // failed, or None for anything else, which block.py then does, or words the
 // refusal of, in the general way.
 #include <torch/csrc/Exceptions.h>
@@ -99,7 +99,31 @@ PyObject* pack(std::initializer_list<Tensor> ts) {
   return out;
 }
 
-void* stream_of(PyObject* o) { return PyLong_AsVoidPtr(o); }
+PyObject *current_device = nullptr, *current_raw_stream = nullptr;  // torch's functions of these names
+
+// The stream of a call: the handle that is given, or, for None, the current one,
+// if the current device is the tensors'.  False: the general way (no error set).
+bool stream_of(PyObject* o, int64_t dev, void** stream) {
+  if (o != Py_None) {
+    *stream = PyLong_AsVoidPtr(o);
+    return true;
+  }
+  if (!current_device || !current_raw_stream) return false;
+  PyObject* d = PyObject_CallNoArgs(current_device);
+  if (!d) {
+    PyErr_Clear();
+    return false;
+  }
+  PyObject* s = PyLong_AsLongLong(d) == dev ? PyObject_CallOneArg(current_raw_stream, d) : nullptr;
+  Py_DECREF(d);
+  if (!s) {
+    PyErr_Clear();
+    return false;
+  }
+  *stream = PyLong_AsVoidPtr(s);
+  Py_DECREF(s);
+  return true;
+}
 
 // (x, weight, bias, eps, stream)
 PyObject* layer_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -112,15 +136,15 @@ PyObject* layer_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Rows xr;
   at::ScalarType wt = x.scalar_type();
   bool given = false;
-  void *w, *b;
+  void *w, *b, *st;
   if (!rows_of(a[0], x.scalar_type(), M, D, dev, &xr) || !vector_of(a[1], D, dev, x.scalar_type(), &wt, &given, &w) ||
-      !vector_of(a[2], D, dev, x.scalar_type(), &wt, &given, &b))
+      !vector_of(a[2], D, dev, x.scalar_type(), &wt, &given, &b) || !stream_of(a[4], dev, &st))
     return none();
   Tensor y = at::empty({M, D}, x.options());
   Tensor mean = at::empty({M}, x.options().dtype(at::kFloat)), rstd = at::empty({M}, mean.options());
   const int s = swiglu_layer_norm_fwd(xr.p, xr.ld, w, b, y.data_ptr(), D, (float*)mean.data_ptr(),
                                       (float*)rstd.data_ptr(), M, D, PyFloat_AS_DOUBLE(a[3]), dt,
-                                      wt == at::kFloat ? SWIGLU_FP32 : dt, stream_of(a[4]));
+                                      wt == at::kFloat ? SWIGLU_FP32 : dt, st);
   return s == SWIGLU_OK ? pack({y, mean, rstd}) : PyLong_FromLong(s);
   END_HANDLE_TH_ERRORS
 }
@@ -137,12 +161,13 @@ PyObject* layer_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Rows dyr, xr, rr;
   at::ScalarType wt = x.scalar_type();
   bool given = false;
-  void *w, *mean, *rstd;
+  void *w, *mean, *rstd, *st;
   if (!rows_of(a[0], x.scalar_type(), M, D, dev, &dyr) || !rows_of(a[1], x.scalar_type(), M, D, dev, &xr) ||
       !vector_of(a[2], D, dev, x.scalar_type(), &wt, &given, &w) || !dense_of(a[3], at::kFloat, {M}, dev, &mean) ||
       !dense_of(a[4], at::kFloat, {M}, dev, &rstd))
     return none();
   if (a[5] != Py_None && !rows_of(a[5], x.scalar_type(), M, D, dev, &rr)) return none();
+  if (!stream_of(a[7], dev, &st)) return none();
   Tensor dx = at::empty({M, D}, x.options()), dw, db;
   if (w) dw = at::empty({D}, x.options().dtype(wt));
   if (bias) db = at::empty({D}, x.options().dtype(wt));
@@ -151,7 +176,7 @@ PyObject* layer_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int s = swiglu_layer_norm_bwd(dyr.p, dyr.ld, xr.p, xr.ld, w, (const float*)mean, (const float*)rstd, rr.p,
                                       rr.p ? rr.ld : D, dx.data_ptr(), D, w ? dw.data_ptr() : nullptr,
                                       bias ? db.data_ptr() : nullptr, ws.data_ptr(), (size_t)ws.numel(), M, D, dt,
-                                      wt == at::kFloat ? SWIGLU_FP32 : dt, stream_of(a[7]));
+                                      wt == at::kFloat ? SWIGLU_FP32 : dt, st);
   return s == SWIGLU_OK ? pack({dx, dw, db}) : PyLong_FromLong(s);
   END_HANDLE_TH_ERRORS
 }
@@ -188,11 +213,13 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       o[i] = u.data_ptr();
     }
   }
+  void* st;
+  if (!stream_of(a[3], dev, &st)) return none();
   Tensor total = at::empty({}, like.options().dtype(at::kFloat));
   const Tensor ws = workspace(swiglu_clip_grad_norm_workspace(count), like);
   const int s = swiglu_clip_grad_norm(g.data(), apart ? o.data() : nullptr, numel.data(), types.data(), count,
                                       PyFloat_AS_DOUBLE(a[2]), (float*)total.data_ptr(), ws.data_ptr(),
-                                      (size_t)ws.numel(), stream_of(a[3]));
+                                      (size_t)ws.numel(), st);
   return s == SWIGLU_OK ? THPVariable_Wrap(total) : PyLong_FromLong(s);
   END_HANDLE_TH_ERRORS
 }
@@ -207,9 +234,9 @@ PyObject* moe_few(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (x.dim() != 2 || wd.dim() != 3) return none();
   const int64_t M = x.size(0), D = x.size(1), dev = x.get_device();
   const int64_t E = wd.size(0), I = wd.size(1), Dout = wd.size(2);
-  void *xp, *w1, *w2, *wr = nullptr, *ip = nullptr, *gp = nullptr;
+  void *xp, *w1, *w2, *st, *wr = nullptr, *ip = nullptr, *gp = nullptr;
   if (!dense_of(a[0], at::kBFloat16, {M, D}, dev, &xp) || !dense_of(a[2], at::kBFloat16, {E, D, 2 * I}, dev, &w1) ||
-      !dense_of(a[3], at::kBFloat16, {E, I, Dout}, dev, &w2))
+      !dense_of(a[3], at::kBFloat16, {E, I, Dout}, dev, &w2) || !stream_of(a[6], dev, &st))
     return none();
   const bool route = a[1] != Py_None;
   Tensor ids, weights;
@@ -235,7 +262,6 @@ PyObject* moe_few(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor y = at::empty({M, Dout}, x.options());
   const Tensor ws = workspace(route ? swiglu_moe_few_layer_workspace(M, D, I, Dout, E, k)
                                     : swiglu_moe_few_workspace(M, D, I, Dout, E, k), x);
-  void* st = stream_of(a[6]);
   const int s = route ? swiglu_moe_few_layer(xp, wr, w1, w2, y.data_ptr(), (int32_t*)ip, (float*)gp, ws.data_ptr(),
                                              (size_t)ws.numel(), M, D, I, Dout, E, k, a[5] == Py_True, st)
                       : swiglu_moe_few_fwd(xp, w1, w2, (const int32_t*)ip, (const float*)gp, y.data_ptr(),
@@ -255,4 +281,15 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_host", nullptr, -1, methods, null
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__host(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__host(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (!m) return nullptr;
+  if (PyObject* c = PyImport_ImportModule("torch._C")) {
+    current_device = PyObject_GetAttrString(c, "_cuda_getDevice");
+    PyErr_Clear();
+    current_raw_stream = PyObject_GetAttrString(c, "_cuda_getCurrentRawStream");
+    Py_DECREF(c);
+  }
+  PyErr_Clear();  // without them a call passes its stream
+  return m;
+}
