@@ -148,8 +148,8 @@ def swiglu_layer_norm_bwd_workspace(M, D) -> int:
 
 
 @_launches
-def _layer_norm_bwd(dy, x, weight, mean, rstd=None, dres=None, bias_grad=True, dx=None, dweight=None, dbias=None, ws=None,
-                    stream=None):
+def _layer_norm_bwd(dy, x, weight, mean, rstd=None, dres=None, bias_grad=True, dx=None, dweight=None, dbias=None,
+                    ws=None, stream=None):
     if x.dim() != 2:
         raise ValueError(f"x must have two dimensions, got {tuple(x.shape)}")
     shape, t, dev = x.shape, x.dtype, x.get_device()
@@ -296,7 +296,7 @@ def swiglu_clip_grad_norm(grads, max_norm, outs=None, total=None, ws=None, strea
     max_norm / (total + 1e-6)), total the 2-norm of all of them together, in
     place or into `outs`.  Returns total, a float32 scalar on the GPU: the
     host does not wait."""
-    if stream is None and total is None and ws is None:
+    if stream is None and total is None and ws is None and isinstance(max_norm, (float, int)):
         got = _host().clip_grad_norm(grads, outs, float(max_norm), None)
         if got is not None:
             return _native("swiglu_clip_grad_norm", got)
