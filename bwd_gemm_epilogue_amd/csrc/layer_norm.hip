@@ -382,6 +382,123 @@ __global__ void __launch_bounds__(THREADS) ln_bwd_kernel(const BwdArgs a) {
   }
 }
 
+// A few rows in one launch: workgroups 0 .. M - 1 make a row of dx each, the
+// others the sums of 64 columns each, over all rows, from x and dy themselves
+// (read a second time, from the cache), so that nothing has to wait for anything.
+template <class T, class W, int NV>
+__global__ void __launch_bounds__(256) ln_bwd_few_kernel(const BwdArgs a, W* dw, W* db) {
+  constexpr int VEC = Vec<T>::N;
+  __shared__ float red[2][4], sums[2][256 / (64 / VEC)][64];
+  const int D = a.D, M = (int)a.M;
+  if ((int)blockIdx.x < M) {
+    const int tl = threadIdx.x, nvec = D / VEC, tail = nvec * VEC + tl;
+    const int64_t row = blockIdx.x;
+    const T* x = (const T*)a.x + row * a.ldx;
+    const T* dy = (const T*)a.dy + row * a.lddy;
+    const T* rs = (const T*)a.dres + row * a.lddres;
+    T* dx = (T*)a.dx + row * a.lddx;
+    const W* w = (const W*)a.w;
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float g[NV][VEC], xh[NV][VEC], gt = 0.0f, xt = 0.0f, s1 = 0.0f, s2 = 0.0f;
+    typename Vec<T>::type r[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = tl + i * 256;
+      if (v < nvec) {
+        const auto xr = load_vec(x + v * VEC), yr = load_vec(dy + v * VEC);
+        if (a.dres) r[i] = load_vec(rs + v * VEC);
+        if (w) load_floats<VEC>(w + v * VEC, g[i]);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          g[i][e] = w ? (float)yr[e] * g[i][e] : (float)yr[e];
+          xh[i][e] = ((float)xr[e] - mean) * rstd;
+          s1 += g[i][e];
+          s2 = __builtin_fmaf(g[i][e], xh[i][e], s2);
+        }
+      }
+    }
+    if (tail < D) {
+      gt = (float)dy[tail] * (w ? (float)w[tail] : 1.0f);
+      xt = ((float)x[tail] - mean) * rstd;
+      s1 += gt;
+      s2 = __builtin_fmaf(gt, xt, s2);
+    }
+    const float m1 = row_sum<256>(s1, red[0]) * a.inv_d, m2 = row_sum<256>(s2, red[1]) * a.inv_d;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = tl + i * 256;
+      if (v < nvec) {
+        typename Vec<T>::type o;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          float u = __builtin_fmaf(-xh[i][e], m2, g[i][e] - m1) * rstd;
+          if (a.dres) u += (float)r[i][e];
+          o[e] = (T)u;
+        }
+        store_vec(dx + v * VEC, o);
+      }
+    }
+    if (tail < D) {
+      float u = (gt - m1 - xt * m2) * rstd;
+      if (a.dres) u += (float)rs[tail];
+      dx[tail] = (T)u;
+    }
+    return;
+  }
+  // lane -> a vector of columns and one of SUBS rows; the last vector of a row
+  // overlaps the one before it where D is no multiple (D >= VEC)
+  constexpr int LANES = 64 / VEC, SUBS = 256 / LANES;
+  const int c0 = ((int)blockIdx.x - M) * 64 + (threadIdx.x % LANES) * VEC, cs = c0 < D - VEC ? c0 : D - VEC;
+  const int sub = threadIdx.x / LANES;
+  const T* x = (const T*)a.x + cs;
+  const T* dy = (const T*)a.dy + cs;
+  float sw[VEC], sb[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) sw[e] = sb[e] = 0.0f;
+  for (int q = sub; q < M; q += 4 * SUBS) {
+    typename Vec<T>::type xv[4], yv[4];
+    float mean[4], rstd[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t row = q + u * SUBS < M ? q + u * SUBS : M - 1;
+      xv[u] = load_vec(x + row * a.ldx);
+      yv[u] = load_vec(dy + row * a.lddy);
+      mean[u] = a.mean[row];
+      rstd[u] = a.rstd[row];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (q + u * SUBS < M) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float d = (float)yv[u][e];
+          sw[e] = __builtin_fmaf(d, ((float)xv[u][e] - mean[u]) * rstd[u], sw[e]);
+          sb[e] += d;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    // this lane's place in the workgroup's 64 columns; the overlap is left out
+    const int at = cs + e - ((int)blockIdx.x - M) * 64;
+    if (cs + e >= c0 && at < 64) {
+      sums[0][sub][at] = sw[e];
+      sums[1][sub][at] = sb[e];
+    }
+  }
+  __syncthreads();
+  const int c = ((int)blockIdx.x - M) * 64 + (int)(threadIdx.x & 63);
+  W* out = threadIdx.x < 64 ? dw : db;
+  if (threadIdx.x < 128 && c < D && out) {
+    const float(*p)[64] = sums[threadIdx.x >> 6];
+    float t = 0.0f;
+#pragma unroll
+    for (int u = 0; u < SUBS; ++u) t += p[u][threadIdx.x & 63];
+    out[c] = (W)t;
+  }
+}
+
 // dx of a row that does not fit the registers of a workgroup
 template <class T, class W>
 __global__ void __launch_bounds__(256) ln_bwd_wide_kernel(const BwdArgs a) {
@@ -506,6 +623,17 @@ using namespace swb;
 
 constexpr int64_t kMaxNormDim = (int64_t)1 << 20;
 constexpr int64_t kLaunchRows = (int64_t)1 << 23;
+// The backward in one launch (D at least a vector), whose column sums read x and dy
+// again.  us, one launch against two: bf16 64 x 4096
+// 4.4 / 7.6, 256 x 512 4.7 / 7.4, 512 x 2048 7.2 / 8.3, 640 x 2048 9.1 / 8.7; fp32
+// 256 x 2048 6.3 / 7.5, 333 x 2048 9.0 / 8.0.  Wider rows make the other way's
+// partial sums dearer: fp32 420 x 8191 14.7 / 15.4, 512 x 8191 17.3 / 15.7; bf16
+// 640 x 8191 14.1 / 16.3.
+constexpr int64_t kFewWidth = 256 * 32;
+bool few_rows(int64_t M, int64_t D, int es) {
+  return D >= 16 / es && D <= kFewWidth && M * es <= (D > 4096 ? 1536 : 1024);
+}
+
 constexpr int64_t kBwdGroups = 256;  // workgroups of the row pass at most, and parts of dw and db
 
 template <class T, class W, int G, int E>
@@ -558,6 +686,20 @@ int bwd_go(const BwdArgs& a, int64_t* parts, hipStream_t st) {
 // 38.4; a wave with 32: 40.9), to 4096 256 threads with 16 (11136 x 3584: 62.6;
 // two rows 65.6, 32 elements 68.4), to 8192 512 threads with 16 (1000 x 6000:
 // 15.2; 256 with 32: 17.2).
+template <class T, class W, int E>
+int bwd_few(const BwdArgs& a, void* dw, void* db, hipStream_t st) {
+  const int64_t cols = dw || db ? (a.D + 63) / 64 : 0;
+  hipLaunchKernelGGL((ln_bwd_few_kernel<T, W, E / Vec<T>::N>), dim3((unsigned)(a.M + cols)), dim3(256), 0, st, a, (W*)dw,
+                     (W*)db);
+  return launch_status();
+}
+template <class T, class W>
+int bwd_few_typed(const BwdArgs& a, void* dw, void* db, hipStream_t st) {
+  if (a.D <= 256 * 8) return bwd_few<T, W, 8>(a, dw, db, st);
+  if (a.D <= 256 * 16) return bwd_few<T, W, 16>(a, dw, db, st);
+  return bwd_few<T, W, 32>(a, dw, db, st);
+}
+
 template <class T, class W>
 int bwd_typed(const BwdArgs& a, int64_t* parts, hipStream_t st) {
   if (a.D <= 64 * 8) return bwd_go<T, W, 64, 8, 512>(a, parts, st);
@@ -695,6 +837,10 @@ int swiglu_layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t l
   const BwdArgs a{dy,   x,   weight, dres,   mean, rstd,   dx, want ? (float*)ws : nullptr,
                   lddy, ldx, lddres, lddx,   M,    (int)D, dbias ? 1 : 0,
                   (float)(1.0 / (double)D)};
+  if (few_rows(M, D, es))
+    return by_type(dtype, wdtype, [&](auto t, auto w) {
+      return bwd_few_typed<decltype(t), decltype(w)>(a, dweight, dbias, st);
+    });
   int64_t parts = 0;
   SW_TRY(by_type(dtype, wdtype,
                  [&](auto t, auto w) { return bwd_typed<decltype(t), decltype(w)>(a, &parts, st); }));

@@ -129,6 +129,20 @@ def test_many_rows(M, D, t):
     check_bwd(x, w, mean.cpu(), rstd.cpu(), dy, res, dx, dw, db)
 
 
+# rows past those of the one-launch backward, of every width that it is dispatched
+# by, odd ones and ones shorter than a vector; and the last rows that it takes
+@pytest.mark.parametrize("t,wt", COMBOS)
+@pytest.mark.parametrize("M,D", [(520, 3), (600, 9), (521, 513), (523, 1025), (515, 2047), (517, 4093), (777, 5001), (512, 515),
+                                 (256, 4096), (257, 77), (300, 7)])
+def test_rows_around_the_one_launch_backward(M, D, t, wt):
+    x, w, b, dy, res = make(M, D, TYPES[t], TYPES[wt])
+    X, W, B, DY, R = cuda(x, w, b, dy, res)
+    _, mean, rstd = sw.swiglu_layer_norm_fwd(X, W, B, EPS)
+    for dres, bias in ((None, True), (R, False)):
+        dx, dw, db = sw.swiglu_layer_norm_bwd(DY, X, W, mean, rstd, dres=dres, bias_grad=bias)
+        check_bwd(x, w, mean.cpu(), rstd.cpu(), dy, None if dres is None else res, dx, dw, db)
+
+
 @pytest.mark.parametrize("weight,bias", [(False, False), (True, False), (False, True)])
 @pytest.mark.parametrize("D", [300, 6000, 17001])
 def test_without_weight_or_bias(D, weight, bias):
