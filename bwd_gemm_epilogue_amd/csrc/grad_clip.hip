@@ -25,6 +25,12 @@ constexpr int kTensors = 128;   // of one table: 29 bytes each within 4 KB of ar
 // 626, 619, 600 us to clip 1.23 GB.
 constexpr int kGroups = 4096;
 constexpr int kSumParts = 2048;
+// One launch (grad_clip_small_kernel) up to these.  us, one launch against two, into
+// new outputs and in place: bf16 4 x 2048 elements 8.0:10.5 and 7.1:9.5, 4 x 16384
+// 9.0:9.7 and 8.4:11.6, 32 x 2048 13.6:16.5 and 10.9:13.7; past them bf16 4 x 24576
+// 11.4:9.8 and 10.5:9.6, fp32 4 x 16384 10.9:9.5 and 7.4:9.3.
+constexpr int kSmallChunks = 32;  // of 2048 elements
+constexpr int64_t kSmallBytes = 1 << 17;
 
 struct Table {
   const void* in[kTensors];
@@ -73,19 +79,20 @@ __device__ __forceinline__ Piece piece_of(const Table* ts, int tables, int c) {
   return piece_of(ts[__builtin_amdgcn_readfirstlane(k)], c);
 }
 
-template <class T>
-__device__ __forceinline__ double square_sum(const T* p, int n) {
+// by THREADS threads, this one the tid-th of them
+template <class T, int THREADS>
+__device__ __forceinline__ double square_sum(const T* p, int n, int tid) {
   constexpr int VEC = Vec<T>::N, U = 4;
   const int nvec = n / VEC;
   double s[2] = {0.0, 0.0};
-  for (int v0 = threadIdx.x; v0 < nvec; v0 += 256 * U) {
+  for (int v0 = tid; v0 < nvec; v0 += THREADS * U) {
     typename Vec<T>::type r[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (v0 + 256 * u < nvec) r[u] = load_vec(p + (int64_t)(v0 + 256 * u) * VEC);
+      if (v0 + THREADS * u < nvec) r[u] = load_vec(p + (int64_t)(v0 + THREADS * u) * VEC);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (v0 + 256 * u < nvec) {
+      if (v0 + THREADS * u < nvec) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const double g = (double)(float)r[u][e];
@@ -94,12 +101,19 @@ __device__ __forceinline__ double square_sum(const T* p, int n) {
       }
     }
   }
-  const int tail = nvec * VEC + (int)threadIdx.x;
+  const int tail = nvec * VEC + tid;
   if (tail < n) {
     const double g = (double)(float)p[tail];
     s[0] = __builtin_fma(g, g, s[0]);
   }
   return s[0] + s[1];
+}
+
+template <int THREADS>
+__device__ __forceinline__ double square_piece(const Piece& p, int tid) {
+  if (p.type == SWIGLU_FP32) return square_sum<float, THREADS>((const float*)p.in + p.at, p.n, tid);
+  if (p.type == SWIGLU_BF16) return square_sum<bf16_t, THREADS>((const bf16_t*)p.in + p.at, p.n, tid);
+  return square_sum<fp16_t, THREADS>((const fp16_t*)p.in + p.at, p.n, tid);
 }
 
 template <int WAVES>
@@ -126,9 +140,7 @@ __global__ void __launch_bounds__(256) grad_norm_kernel(const Table t, const Tab
     Piece p;
     if constexpr (FAR) p = piece_of(ts, tables, c);
     else p = piece_of(t, c);
-    if (p.type == SWIGLU_FP32) s += square_sum((const float*)p.in + p.at, p.n);
-    else if (p.type == SWIGLU_BF16) s += square_sum((const bf16_t*)p.in + p.at, p.n);
-    else s += square_sum((const fp16_t*)p.in + p.at, p.n);
+    s += square_piece<256>(p, threadIdx.x);
   }
   s = group_sum<4>(s, red);
   if (threadIdx.x == 0) part[blockIdx.x] = s;
@@ -140,6 +152,10 @@ struct Clip {
   double total;
   float factor;
 };
+__device__ __forceinline__ Clip clip_from(double squares, double max_norm) {
+  const double norm = __builtin_sqrt(squares), q = max_norm / (norm + 1e-6);
+  return {norm, q < 1.0 || q != q ? (float)q : 1.0f};
+}
 template <int THREADS, int N>
 __device__ __forceinline__ Clip clip_of(const double* __restrict__ part, int parts, double max_norm, double* red) {
   double v[N / THREADS], s = 0.0;
@@ -150,9 +166,7 @@ __device__ __forceinline__ Clip clip_of(const double* __restrict__ part, int par
   }
 #pragma unroll
   for (int u = 0; u < N / THREADS; ++u) s += v[u];
-  s = group_sum<THREADS / 64>(s, red);
-  const double norm = __builtin_sqrt(s), q = max_norm / (norm + 1e-6);
-  return {norm, q < 1.0 || q != q ? (float)q : 1.0f};
+  return clip_from(group_sum<THREADS / 64>(s, red), max_norm);
 }
 __global__ void __launch_bounds__(1024) grad_total_kernel(const double* __restrict__ part, int parts, double max_norm,
                                                           float* total, float* factor) {
@@ -164,26 +178,34 @@ __global__ void __launch_bounds__(1024) grad_total_kernel(const double* __restri
   }
 }
 
-template <class T>
-__device__ __forceinline__ void scale(const T* p, T* o, int n, float f) {
+template <class T, int THREADS>
+__device__ __forceinline__ void scale(const T* p, T* o, int n, float f, int tid) {
   constexpr int VEC = Vec<T>::N, U = 4;
   const int nvec = n / VEC;
-  for (int v0 = threadIdx.x; v0 < nvec; v0 += 256 * U) {
+  for (int v0 = tid; v0 < nvec; v0 += THREADS * U) {
     typename Vec<T>::type r[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (v0 + 256 * u < nvec) r[u] = last_vec(p + (int64_t)(v0 + 256 * u) * VEC);
+      if (v0 + THREADS * u < nvec) r[u] = last_vec(p + (int64_t)(v0 + THREADS * u) * VEC);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (v0 + 256 * u < nvec) {
+      if (v0 + THREADS * u < nvec) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) r[u][e] = (T)((float)r[u][e] * f);
-        stream_vec(o + (int64_t)(v0 + 256 * u) * VEC, r[u]);
+        stream_vec(o + (int64_t)(v0 + THREADS * u) * VEC, r[u]);
       }
     }
   }
-  const int tail = nvec * VEC + (int)threadIdx.x;
+  const int tail = nvec * VEC + tid;
   if (tail < n) o[tail] = (T)((float)p[tail] * f);
+}
+
+// the same for a piece of any type
+template <int THREADS>
+__device__ __forceinline__ void scale_piece(const Piece& p, float f, int tid) {
+  if (p.type == SWIGLU_FP32) scale<float, THREADS>((const float*)p.in + p.at, (float*)p.out + p.at, p.n, f, tid);
+  else if (p.type == SWIGLU_BF16) scale<bf16_t, THREADS>((const bf16_t*)p.in + p.at, (bf16_t*)p.out + p.at, p.n, f, tid);
+  else scale<fp16_t, THREADS>((const fp16_t*)p.in + p.at, (fp16_t*)p.out + p.at, p.n, f, tid);
 }
 
 // A workgroup's chunks are those that it had in the norm, from the last to the
@@ -214,9 +236,26 @@ __global__ void __launch_bounds__(256) grad_scale_kernel(const Table t, const Ta
     if constexpr (FAR) p = piece_of(ts, tables, c);
     else p = piece_of(t, c);
     if (f == 1.0f && p.in == p.out) continue;  // in place and unchanged
-    if (p.type == SWIGLU_FP32) scale((const float*)p.in + p.at, (float*)p.out + p.at, p.n, f);
-    else if (p.type == SWIGLU_BF16) scale((const bf16_t*)p.in + p.at, (bf16_t*)p.out + p.at, p.n, f);
-    else scale((const fp16_t*)p.in + p.at, (fp16_t*)p.out + p.at, p.n, f);
+    scale_piece<256>(p, f, threadIdx.x);
+  }
+}
+
+// A few chunks in one launch of one workgroup: a wave to a chunk, for the norm and
+// then, with the factor in every thread, for the scaling.
+__global__ void __launch_bounds__(1024) grad_clip_small_kernel(const Table t, int chunks, double max_norm, int norm_only,
+                                                               float* total) {
+  __shared__ double red[16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  double s = 0.0;
+  for (int c = wave; c < chunks; c += 16) s += square_piece<64>(piece_of(t, c), lane);
+  s = group_sum<16>(s, red);
+  const Clip clip = clip_from(s, max_norm);
+  if (threadIdx.x == 0) *total = (float)clip.total;
+  if (norm_only) return;
+  for (int c = wave; c < chunks; c += 16) {
+    const Piece p = piece_of(t, c);
+    if (clip.factor == 1.0f && p.in == p.out) continue;
+    scale_piece<64>(p, clip.factor, lane);
   }
 }
 
@@ -280,11 +319,12 @@ int swiglu_clip_grad_norm(const void* const* grads, void* const* outs, const int
   if (n < 0 || !(max_norm >= 0.0)) return SWIGLU_ERR_SHAPE;
   if (n > kMaxTensors) return SWIGLU_ERR_UNSUPPORTED;
   if (n > 0 && (!grads || !numels || !dtypes)) return SWIGLU_ERR_NULL;
-  int64_t elements = 0;
+  int64_t elements = 0, bytes = 0;
   for (int64_t i = 0; i < n; ++i) {
     if (numels[i] < 0) return SWIGLU_ERR_SHAPE;
     if (numels[i] > kMaxElements || !dtype_ok(dtypes[i])) return SWIGLU_ERR_UNSUPPORTED;
     elements += numels[i];
+    bytes += numels[i] * elem_size(dtypes[i]);
   }
   if (elements > kMaxElements) return SWIGLU_ERR_UNSUPPORTED;
   const bool norm_only = max_norm == __builtin_inf();
@@ -305,10 +345,10 @@ int swiglu_clip_grad_norm(const void* const* grads, void* const* outs, const int
   if (!spans) return SWIGLU_ERR_HIP;
   int64_t ns = 0;
   for (int64_t i = 0; i < n; ++i) {
-    const uintptr_t bytes = (uintptr_t)numels[i] * elem_size(dtypes[i]);
+    const uintptr_t size = (uintptr_t)numels[i] * elem_size(dtypes[i]);
     const bool in_place = !outs || outs[i] == grads[i];
-    spans[ns++] = {(uintptr_t)grads[i], (uintptr_t)grads[i] + bytes, in_place && !norm_only};
-    if (!in_place) spans[ns++] = {(uintptr_t)outs[i], (uintptr_t)outs[i] + bytes, true};
+    spans[ns++] = {(uintptr_t)grads[i], (uintptr_t)grads[i] + size, in_place && !norm_only};
+    if (!in_place) spans[ns++] = {(uintptr_t)outs[i], (uintptr_t)outs[i] + size, true};
   }
   spans[ns++] = {(uintptr_t)total, (uintptr_t)total + 4, true};
   spans[ns++] = {(uintptr_t)ws, (uintptr_t)ws + need, true};
@@ -342,6 +382,10 @@ int swiglu_clip_grad_norm(const void* const* grads, void* const* outs, const int
     }
   }
   const int chunks = (int)c, groups = chunks < kGroups ? chunks : kGroups;
+  if (tables == 1 && chunks <= kSmallChunks && bytes <= kSmallBytes) {
+    hipLaunchKernelGGL(grad_clip_small_kernel, dim3(1), dim3(1024), 0, st, t, chunks, max_norm, norm_only ? 1 : 0, total);
+    return launch_status();
+  }
   if (groups > 0) {
     auto k = tables > 1 ? grad_norm_kernel<true> : grad_norm_kernel<false>;
     hipLaunchKernelGGL(k, dim3((unsigned)groups), dim3(256), 0, st, t, (const Table*)tabs, tables, chunks, part);

@@ -233,3 +233,73 @@ def test_refusals_on_the_gpu():
                 lambda: sw.swiglu_clip_grad_norm([g[:60]], 1.0, outs=[g[4:]])):
         with pytest.raises(sw.SwiGLUError):
             bad()
+
+
+# 31 to 33 chunks of 2048 elements, one launch on one side and two on the other
+EDGE = [
+    ([2048 * 32], [BF16]), ([2048 * 32 + 1], [BF16]), ([2048 * 32, 0, 0], [FP32]), ([2048 * 31 + 5, 1], [FP16, FP32]),
+    ([2048 * 31, 1, 1], [FP32]), ([1, 2047, 2049] * 8, [BF16, FP32, FP16]), ([3] * 32, [FP16]), ([3] * 33, [FP16, BF16]),
+    ([0] * 96 + [11] * 32, [BF16]), ([4095, 4097] * 7 + [2048], [FP32, FP16]), ([9] * 32 + [0] * 97, [FP32]),
+]
+
+
+@pytest.mark.parametrize("k", range(len(EDGE)))
+def test_sizes_around_the_one_launch(k):
+    grads = make(*EDGE[k], seed=100 + k)
+    max_norm = 0.3 * norm64(grads)
+    flat = [torch.full((g.numel() + 2,), 9.0, dtype=g.dtype, device="cuda") for g in grads]
+    d = [f[1:-1].copy_(g) for f, g in zip(flat, grads)]          # off 16-byte boundaries
+    assert abs(float(sw.swiglu_grad_norm(d)) - norm64(grads)) <= 2 * E32 * norm64(grads)
+    outs = [torch.full_like(g, 3.0) for g in d]
+    total = sw.swiglu_clip_grad_norm(d, max_norm, outs=outs)
+    check(grads, outs, total, max_norm)
+    check(grads, d, sw.swiglu_clip_grad_norm(d, 9.0 * max_norm), 9.0 * max_norm)   # not clipped
+    check(grads, d, sw.swiglu_clip_grad_norm(d, max_norm), max_norm)
+    assert all(bool(f[0] == 9) and bool(f[-1] == 9) for f in flat)
+
+
+@pytest.mark.parametrize("pad", [0, 2048 * 40])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_a_bad_gradient_in_one_launch_and_in_two(bad, pad):
+    """An infinite total: the factor is 0, finite gradients become 0 and the
+    infinite one NaN.  A NaN total leaves NaN everywhere."""
+    d = [torch.ones(77, device="cuda"), torch.ones(2051 + pad, dtype=BF16, device="cuda")]
+    d[1][2050] = bad
+    total = float(sw.swiglu_clip_grad_norm(d, 1.0))
+    rest = [d[0], d[1][:2050], d[1][2051:]]
+    assert bool(d[1][2050].isnan())
+    if math.isnan(bad):
+        assert math.isnan(total) and all(bool(r.isnan().all()) for r in rest)
+    else:
+        assert total == math.inf and all(bool((r == 0).all()) for r in rest)
+
+
+def test_small_set_in_a_graph():
+    grads = make([33, 2048, 700], [BF16, FP32], seed=12)
+    want = 0.2 * norm64(grads)
+    d = [g.cuda() for g in grads]
+    outs = [torch.empty_like(g) for g in d]
+    sw.swiglu_clip_grad_norm(d, want, outs=outs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        total = sw.swiglu_clip_grad_norm(d, want, outs=outs)
+    for k in range(4):
+        for a, b in zip(d, grads):
+            a.copy_(b * 2 ** k)
+        graph.replay()
+        now = [g * 2 ** k for g in grads]
+        check(now, outs, total, want)
+        got = [o.clone() for o in outs]
+        sw.swiglu_clip_grad_norm(d, want, outs=outs)
+        assert all(torch.equal(a, b) for a, b in zip(got, outs))
+
+
+@pytest.mark.parametrize("n", [2 ** 15 - 1, 2 ** 15, 2 ** 15 + 1])
+def test_fp32_sizes_around_the_one_launch(n):
+    grads = make([n - 7, 7], [FP32], seed=n)
+    d = [g.cuda() for g in grads]
+    outs = [torch.full_like(g, 3.0) for g in d]
+    max_norm = 0.4 * norm64(grads)
+    check(grads, outs, sw.swiglu_clip_grad_norm(d, max_norm, outs=outs), max_norm)
+    check(grads, d, sw.swiglu_clip_grad_norm(d, max_norm), max_norm)
