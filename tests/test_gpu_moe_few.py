@@ -285,3 +285,44 @@ def test_refusals_on_the_gpu():
                 lambda: sw.swiglu_moe_few_layer(x.repeat(17, 1), Wr, W1, Wd, 2)):
         with pytest.raises(sw.SwiGLUError):
             bad()
+
+
+@pytest.mark.parametrize("E", [1, 7, 8, 63, 64, 65, 128, 129, 200, 257, 959, 961, 1023, 1024])
+@pytest.mark.parametrize("k", [1, 3, 15, 63, 64])
+def test_choice_over_groups_of_experts(E, k):
+    """Ranks within groups of 64 experts and over them: distinct logits, equal
+    ones within a group and across groups, and infinite and NaN ones."""
+    k = min(k, E)
+    g = torch.Generator().manual_seed(E * 64 + k)
+    x = torch.randn(9, 128, generator=g).to(torch.bfloat16)
+    Wr = torch.randn(128, E, generator=g).to(torch.bfloat16)
+    some = torch.randint(0, E, (2 * E,), generator=g)
+    twice = Wr[:, some[:E] % max(1, E // 3)].contiguous()     # columns that come several times
+    for tokens in (1, 9):
+        for w in (Wr, twice):
+            for renorm in (True, False):
+                ids, got = sw.swiglu_moe_route(x[:tokens].cuda(), w.cuda(), k, renormalize=renorm)
+                rid, rw = route64(x[:tokens], w, k, renorm)
+                assert torch.equal(ids.cpu().long(), rid)
+                assert ((got.cpu().double() - rw).abs() <= 1.001 * E32 * rw + 1e-45).all()
+    # the layer's own choice is the router's
+    W1, Wd = (torch.zeros(E, 128 if i == 0 else 64, 128, dtype=torch.bfloat16, device="cuda") for i in range(2))
+    for w in (Wr, twice):
+        y, ids, got = sw.swiglu_moe_few_layer(x[:1].cuda(), w.cuda(), W1, Wd, k)
+        i2, w2 = sw.swiglu_moe_route(x[:1].cuda(), w.cuda(), k)
+        assert torch.equal(ids, i2) and torch.equal(got, w2) and not y.any()
+    # experts whose logits are -inf or NaN come last, in order of number
+    low = Wr.clone()
+    bad = sorted(set(some[E:E + max(1, E // 5)].tolist()))
+    low[:, bad] = 0.0
+    low[0, bad] = float("-inf")
+    x2 = x.clone()
+    x2[:, 0] = 1.0
+    ids, got = sw.swiglu_moe_route(x2.cuda(), low.cuda(), k)
+    l = x2.double() @ low.double()
+    l[:, bad] = -float("inf")
+    rid = torch.sort(l, dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(ids.cpu().long(), rid)
+    x2[:, 0] = float("nan")                                   # every logit NaN
+    ids, got = sw.swiglu_moe_route(x2.cuda(), Wr.cuda(), k)
+    assert torch.equal(ids.cpu(), torch.arange(k, dtype=torch.int32).expand(9, k)) and got.isnan().all()
