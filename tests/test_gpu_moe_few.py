@@ -326,3 +326,18 @@ def test_choice_over_groups_of_experts(E, k):
     x2[:, 0] = float("nan")                                   # every logit NaN
     ids, got = sw.swiglu_moe_route(x2.cuda(), Wr.cuda(), k)
     assert torch.equal(ids.cpu(), torch.arange(k, dtype=torch.int32).expand(9, k)) and got.isnan().all()
+
+
+@pytest.mark.parametrize("M,I,Dout,E,k", [(1, 512, 64, 70, 64), (2, 576, 192, 40, 31), (1, 2048, 64, 9, 5),
+                                          (7, 1024, 128, 2, 1), (3, 64, 320, 64, 47), (64, 128, 64, 20, 16)])
+def test_many_terms_of_a_result(M, I, Dout, E, k):
+    """Choices times parts of I: from one term to hundreds, some of them void."""
+    x, _, W1, Wd = make(M, 64, I, Dout, E, seed=3)
+    g = torch.Generator().manual_seed(k)
+    ids = torch.randint(0, E, (M, k), generator=g, dtype=torch.int32)
+    ids[torch.rand(M, k, generator=g) < 0.2] = E
+    w = torch.randn(M, k, generator=g)
+    ws = torch.full((sw.swiglu_moe_few_workspace(M, 64, I, Dout, E, k),), 255, dtype=torch.uint8, device="cuda")
+    y = sw.swiglu_moe_few_fwd(x.cuda(), W1.cuda(), Wd.cuda(), ids.cuda(), w.cuda(), ws=ws)
+    check(y, x, W1, Wd, ids, w)
+    assert torch.equal(y, sw.swiglu_moe_few_fwd(x.cuda(), W1.cuda(), Wd.cuda(), ids.cuda(), w.cuda()))
