@@ -17,7 +17,8 @@
 //   * gate/up: a workgroup finds its expert among the ids, gathers the expert's
 //     rows, and streams one block of 128 columns of W1 (64 of left, 64 of gate);
 //   * down: the same on W_down, 128 columns; where K of the gate/up was split,
-//     it first makes h of its rows from the parts;
+//     it first makes h of its rows from the parts (past 16 rows a launch between
+//     does);
 //   * combine: the weighted sum of the rows' results, in a fixed order.  (By the
 //     last workgroup of a block of columns to arrive it took as long for a token
 //     and longer for more: 134 -> 149 us at 32, 166 with device-scope fences.)
@@ -294,6 +295,33 @@ __device__ __forceinline__ void halves(float h, uint16_t& hi, uint16_t& lo) {
   lo = __builtin_bit_cast(uint16_t, (bf16_t)(__builtin_fabsf((float)top) < __builtin_inff() ? rest : 0.0f));
 }
 
+// Four values of a row's h from its parts, [splits][P][2 I]: p is the first of them
+// in the first part, gate half I behind left.
+__device__ __forceinline__ void h_of_parts(const float* p, int splits, int P, int I, uint16_t (&hi)[4],
+                                           uint16_t (&lo)[4]) {
+  f32x4 left = {}, gate = {};
+  for (int u = 0; u < splits; ++u) {
+    left += *(const f32x4*)(p + (int64_t)u * P * 2 * I);
+    gate += *(const f32x4*)(p + (int64_t)u * P * 2 * I + I);
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) halves(swg::swiglu_h(left[v], gate[v]), hi[v], lo[v]);
+}
+
+// h of all rows, its two halves one after the other, where it is not the down
+// launch that makes it.
+__global__ void __launch_bounds__(64) few_h_kernel(const float* __restrict__ part, int splits, int P, int I,
+                                                   uint16_t* __restrict__ h) {
+  const int64_t per = I / 4, t = (int64_t)blockIdx.x * 64 + threadIdx.x;
+  if (t >= P * per) return;
+  const int64_t p = t / per, c = t % per * 4;
+  uint16_t hi[4], lo[4];
+  h_of_parts(part + p * 2 * I + c, splits, P, I, hi, lo);
+  uint16_t* o = h + p * I + c;
+  *(uint2*)o = uint2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
+  *(uint2*)(o + (int64_t)P * I) = uint2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};
+}
+
 // Loads of the main loop are buffer loads: a scalar descriptor, a lane offset
 // held for the whole loop and a scalar offset.  (As global loads the compiler
 // kept a 64-bit address in registers for each of a step's rows, which spilled.)
@@ -422,14 +450,8 @@ __global__ void __launch_bounds__(WAVES * 64, AHEAD > 2 ? 1 : NT > 1 ? 2 : KIND 
       const int q = min(q0 + tid, total - 1);
       const int r = q / (width / 4), c = (q - r * (width / 4)) * 4;
       const float* p = a.gate_part + (int64_t)row_of(r) * 2 * a.K + s0 * 32 + c;
-      f32x4 left = {}, gate = {};
-      for (int u = 0; u < a.gate_splits; ++u) {
-        left += *(const f32x4*)(p + (int64_t)u * a.P * 2 * a.K);
-        gate += *(const f32x4*)(p + (int64_t)u * a.P * 2 * a.K + a.K);
-      }
       uint16_t hi[4], lo[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) halves(swg::swiglu_h(left[v], gate[v]), hi[v], lo[v]);
+      h_of_parts(p, a.gate_splits, a.P, a.K, hi, lo);
       uint16_t* o = hs + r * hpitch + c;
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
@@ -661,10 +683,16 @@ int few_splits(int64_t blocks, int64_t slots, int64_t K) {
 struct Plan {
   int64_t P, slots, blocks2;
   int s1, s2;              // parts of D in the gate/up, of I in the down product
+  bool parts;              // h is made by the down launch
   size_t h, part1, part2;  // bytes
   size_t bytes() const { return h + part1 + part2; }
 };
 
+// Where the down launch cannot make h, a split gate/up costs a launch more
+// (few_h_kernel) and is taken past this many rows of W1.  us, split and whole: 20 tokens
+// over 4 experts of 1024 x 256 20.6 and 20.4, 20 over 8 of 512 x 512 20.7 and 19.3; 32 over
+// 8 of 2048 x 512 26.3 and 32.9, 64 over 4 of 4096 x 1024 43.6 and 66.2.
+constexpr int64_t kApartDepth = 1024;
 Plan plan_few(int64_t M, int64_t D, int64_t I, int64_t Dout, int64_t E, int64_t k) {
   Plan p{};
   p.P = M * k;
@@ -675,8 +703,9 @@ Plan plan_few(int64_t M, int64_t D, int64_t I, int64_t Dout, int64_t E, int64_t 
   p.s2 = few_splits(p.blocks2, p.slots, I);
   // a split gate/up leaves h to the down launch: its rows have to fit there
   const int64_t width = ((I / 32 + p.s2 - 1) / p.s2) * 32;
-  if (p.P > kPartRows || p.P * width > kPartValues) p.s1 = 1;
-  p.h = p.s1 > 1 ? 0 : align256((size_t)(2 * p.P * I * 2));
+  p.parts = p.s1 > 1 && p.P <= kPartRows && p.P * width <= kPartValues;
+  if (!p.parts && D <= kApartDepth) p.s1 = 1;
+  p.h = p.parts ? 0 : align256((size_t)(2 * p.P * I * 2));
   p.part1 = p.s1 > 1 ? align256((size_t)(p.s1 * p.P * 2 * I * 4)) : 0;
   p.part2 = align256((size_t)(p.s2 * p.P * Dout * 4));
   return p;
@@ -777,6 +806,11 @@ int run_experts(const void* x, const void* W1, const void* W_down, int* ids, flo
   a.renorm = renorm;
   const dim3 gate_grid((unsigned)(I / 64), (unsigned)pl.slots, (unsigned)pl.s1);
   SW_TRY(logits ? few_tokens<kGateRoute>(a, M, gate_grid, st) : few_tokens<kGate>(a, M, gate_grid, st));
+  if (pl.s1 > 1 && !pl.parts) {
+    hipLaunchKernelGGL(few_h_kernel, dim3((unsigned)((pl.P * (I / 4) + 63) / 64)), dim3(64), 0, st, (const float*)part1,
+                       pl.s1, (int)pl.P, (int)I, h);
+    SW_TRY(launch_status());
+  }
   a.x = h;
   a.w = (const uint16_t*)W_down;
   a.part = part2;
@@ -786,7 +820,7 @@ int run_experts(const void* x, const void* W1, const void* W_down, int* ids, flo
   a.gate_part = part1;
   a.gate_splits = pl.s1;
   const dim3 down_grid((unsigned)pl.blocks2, (unsigned)pl.slots, (unsigned)pl.s2);
-  SW_TRY((pl.s1 > 1 ? few_go<1, kDownPart>(a, down_grid, st) : few_tokens<kDown>(a, M, down_grid, st)));
+  SW_TRY((pl.parts ? few_go<1, kDownPart>(a, down_grid, st) : few_tokens<kDown>(a, M, down_grid, st)));
   const int64_t waves = (k * pl.s2 + kTermsWave - 1) / kTermsWave;
   hipLaunchKernelGGL(few_combine_kernel, dim3((unsigned)((M * (Dout / 4) + 63) / 64)),
                      dim3(64u * (unsigned)(waves < kCombineWaves ? waves : kCombineWaves)), 0, st,

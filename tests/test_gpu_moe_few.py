@@ -341,3 +341,34 @@ def test_many_terms_of_a_result(M, I, Dout, E, k):
     y = sw.swiglu_moe_few_fwd(x.cuda(), W1.cuda(), Wd.cuda(), ids.cuda(), w.cuda(), ws=ws)
     check(y, x, W1, Wd, ids, w)
     assert torch.equal(y, sw.swiglu_moe_few_fwd(x.cuda(), W1.cuda(), Wd.cuda(), ids.cuda(), w.cuda()))
+
+
+@pytest.mark.parametrize("c", [(17, 1088, 64, 64, 3, 1), (20, 1024, 64, 128, 2, 2), (33, 2112, 192, 64, 4, 2),
+                               (64, 1536, 64, 64, 5, 16), (16, 4096, 128, 192, 2, 2), (64, 1152, 64, 64, 1, 1),
+                               (5, 1088, 4160, 64, 2, 1)], ids=lambda c: "x".join(map(str, c)))
+def test_split_gate_products_of_many_rows(c):
+    """Few workgroups and a long sum: D is split although the down launch cannot
+    hold the rows."""
+    M, D, I, Dout, E, k = c
+    x, _, W1, Wd = make(M, D, I, Dout, E, seed=7)
+    g = torch.Generator().manual_seed(M)
+    ids = torch.randint(0, E, (M, k), generator=g, dtype=torch.int32)
+    ids[0] = -1
+    w = torch.randn(M, k, generator=g)
+    ws = torch.full((sw.swiglu_moe_few_workspace(M, D, I, Dout, E, k),), 255, dtype=torch.uint8, device="cuda")
+    y = sw.swiglu_moe_few_fwd(x.cuda(), W1.cuda(), Wd.cuda(), ids.cuda(), w.cuda(), ws=ws)
+    check(y, x, W1, Wd, ids, w)
+    assert not y[0].any()
+    assert torch.equal(y, sw.swiglu_moe_few_fwd(x.cuda(), W1.cuda(), Wd.cuda(), ids.cuda(), w.cuda()))
+
+
+def test_infinite_h_between_launches():
+    tokens, D, I, N = 20, 2048, 64, 64
+    x = torch.zeros(tokens, D, dtype=torch.bfloat16)
+    x[:, 0], x[:, 1], x[:, 2000] = 3e38, 1.0, 3e38
+    W1, Wd = torch.zeros(2, D, 2 * I, dtype=torch.bfloat16), torch.zeros(2, I, N, dtype=torch.bfloat16)
+    W1[:, 0, 5], W1[:, 2000, 5], W1[:, 1, I + 5] = 1.0, 1.0, 1.0     # left 6e38 over two parts, gate 1
+    Wd[:, 5, 0], Wd[:, 5, 1] = 1.0, -1.0
+    ids = (torch.arange(tokens, dtype=torch.int32) % 2).reshape(tokens, 1)
+    y = sw.swiglu_moe_few_fwd(x.cuda(), W1.cuda(), Wd.cuda(), ids.cuda(), torch.ones(tokens, 1, device="cuda")).cpu()
+    assert (y[:, 0] == float("inf")).all() and (y[:, 1] == -float("inf")).all() and y[:, 2:].isnan().all()
