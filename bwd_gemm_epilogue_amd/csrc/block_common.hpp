@@ -75,14 +75,19 @@ __device__ __forceinline__ float dpp_add(float v) {
   const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false);
   return v + __builtin_bit_cast(float, o);
 }
-// The sum over the 64 lanes, the same value in every lane.  All lanes active.
-// Four steps inside rows of 16 lanes (register-to-register, no LDS), then the
-// four rows by reading one lane of each.
-__device__ __forceinline__ float wave_sum(float v) {
+// The sum over each G lanes of a wave, 8, 16, 32 or 64, the same value in every
+// one of them.  The lanes of a group are all active or none is.  Up to four steps
+// inside rows of 16 lanes (register-to-register, no LDS), then the other row, or
+// the four rows by reading one lane of each.
+template <int G>
+__device__ __forceinline__ float lanes_sum(float v) {
+  static_assert(G == 8 || G == 16 || G == 32 || G == 64);
   v = dpp_add<0xB1>(v);   // quad_perm 1,0,3,2
   v = dpp_add<0x4E>(v);   // quad_perm 2,3,0,1
   v = dpp_add<0x141>(v);  // mirror within 8 lanes
-  v = dpp_add<0x140>(v);  // mirror within 16 lanes
+  if constexpr (G > 8) v = dpp_add<0x140>(v);  // mirror within 16 lanes
+  if constexpr (G == 32) v += __shfl_xor(v, 16, 64);
+  if constexpr (G < 64) return v;
   const int b = __builtin_bit_cast(int, v);
   const float r0 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 0));
   const float r1 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 16));

@@ -9,13 +9,14 @@
 // and, over all rows, dw = sum dy xh, db = sum dy.
 //
 // Both are bound by HBM: every element is read once into registers and written
-// once.  A row belongs to a wave where it is short, to a workgroup where it is
-// wide.  Measured at 11136 x 3584 bf16 with fp32 weights: the forward 24.2 us
+// once.  A row belongs to a part of a wave where it is narrow (up to 256), to a
+// wave where it is short, to a workgroup where it is wide; a backward of few rows
+// is one launch (few_rows).  Measured at 11136 x 3584 bf16 with fp32 weights: the forward 24.2 us
 // (160 MB, 6.6 TB/s: the inputs come in part from the last-level cache, because
 // y is stored past it; with ordinary stores 39.7 us), the backward with the
 // residual branch's gradient 58.7 us (319 MB, 5.4 TB/s, what a copy of that size
-// reaches).  Small calls are bound by their launches: one row of 4096 takes 7 us
-// of the host, 2.5 of the GPU.
+// reaches).  Small calls are bound by their launches: one row of 4096 takes
+// 6.5 us of the host, 2.5 of the GPU.
 #include "block_common.hpp"
 
 namespace swb {
@@ -27,12 +28,12 @@ __device__ __forceinline__ float sum_of(const float* p) {
   for (int i = 1; i < N; ++i) s += p[i];
   return s;
 }
-// The sum over the G threads of a row: a wave, or a whole workgroup of G / 64
-// waves by way of `red`.  `red` is this call's own: a kernel passes another
+// The sum over the G threads of a row: lanes of a wave, or a whole workgroup of G /
+// 64 waves by way of `red`.  `red` is this call's own: a kernel passes another
 // part of it to its next call, so that one barrier is enough.
 template <int G>
 __device__ __forceinline__ float row_sum(float v, float* red) {
-  v = wave_sum(v);
+  v = lanes_sum<G < 64 ? G : 64>(v);
   if constexpr (G > 64) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -72,8 +73,9 @@ __global__ void __launch_bounds__(256) ln_fwd_kernel(const FwdArgs a) {
   __shared__ float red[2][4];
   const int tl = threadIdx.x & (G - 1);
   int64_t row = blockIdx.x;
+  if constexpr (G < 64) row = row * (256 / G) + threadIdx.x / G;
   if constexpr (G == 64) row = row * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (row >= a.M) return;  // a wave's (G = 64: no barrier follows) or the whole workgroup's
+  if (row >= a.M) return;  // a row's lanes (G <= 64: no barrier follows) or the whole workgroup
   const int D = a.D, nvec = D / VEC, tail = nvec * VEC + tl;
   const T* x = (const T*)a.x + row * a.ldx;
   const W *w = (const W*)a.w, *b = (const W*)a.b;
@@ -211,13 +213,14 @@ struct BwdArgs {
 // loads are in flight while a row is worked on (where the registers hold both).
 template <class T, class W, int G, int NV, int THREADS, bool AHEAD>
 __global__ void __launch_bounds__(THREADS) ln_bwd_kernel(const BwdArgs a) {
-  constexpr int VEC = Vec<T>::N, ROWS = THREADS / G, C = NV * VEC, GW = G / 64;
+  constexpr int VEC = Vec<T>::N, ROWS = THREADS / G, C = NV * VEC, GW = G > 64 ? G / 64 : 1;
   typedef typename Vec<T>::type vec;
   __shared__ float red[2][ROWS][2 * GW];
   // ROWS > 1: [ROWS/2][2][C][G] sums of the columns, then [ROWS/2][2][G] of the tail
   __shared__ float acc_lds[ROWS > 1 ? ROWS / 2 * 2 * (C + 1) * G : 1];
   const int tl = threadIdx.x & (G - 1);
-  const int sub = ROWS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / G) : 0;
+  int sub = threadIdx.x / G;
+  if constexpr (G >= 64) sub = __builtin_amdgcn_readfirstlane(sub);
   const int D = a.D, nvec = D / VEC, tail = nvec * VEC + tl;
   const W* w = (const W*)a.w;
   float wf[NV][VEC], dw[NV][VEC], db[NV][VEC], dwt = 0.0f, dbt = 0.0f;
@@ -294,8 +297,8 @@ __global__ void __launch_bounds__(THREADS) ln_bwd_kernel(const BwdArgs a) {
           }
         }
       }
-      s1 = wave_sum(s1);
-      s2 = wave_sum(s2);
+      s1 = lanes_sum<G < 64 ? G : 64>(s1);
+      s2 = lanes_sum<G < 64 ? G : 64>(s2);
     }
     if constexpr (GW > 1) {
       // the two parities' slots in turn: a round's are read before the next
@@ -643,11 +646,16 @@ int fwd_go(const FwdArgs& a, hipStream_t st) {
   return launch_status();
 }
 
-// Threads to a row by its width (us): a wave with 8, 16 or 32 elements a lane up
-// to 2048 (11136 x 2048 bf16: 14.5; a workgroup: 16.5), a workgroup of 256 above
+// Threads to a row by its width (us): 8, 16 or 32 lanes with 8 elements each up to
+// 256 (1048576 x 64 bf16: 50.2, a wave to a row 253; 262144 x 256: 48.3 and 77.6; fp32
+// 524288 x 128: 86.3 and 127), a wave with 8, 16 or 32 elements a lane up to
+// 2048 (11136 x 2048 bf16: 14.5; a workgroup: 16.5), a workgroup of 256 above
 // (11136 x 3584: 24.0; a wave with 64: 25.7; 32 elements to a thread: 29).
 template <class T, class W>
 int fwd_typed(const FwdArgs& a, hipStream_t st) {
+  if (a.D <= 8 * 8) return fwd_go<T, W, 8, 8>(a, st);
+  if (a.D <= 16 * 8) return fwd_go<T, W, 16, 8>(a, st);
+  if (a.D <= 32 * 8) return fwd_go<T, W, 32, 8>(a, st);
   if (a.D <= 64 * 8) return fwd_go<T, W, 64, 8>(a, st);
   if (a.D <= 64 * 16) return fwd_go<T, W, 64, 16>(a, st);
   if (a.D <= 64 * 32) return fwd_go<T, W, 64, 32>(a, st);
@@ -679,13 +687,6 @@ int bwd_go(const BwdArgs& a, int64_t* parts, hipStream_t st) {
   return launch_status();
 }
 
-// Threads to a row by its width, each side measured at two widths or more
-// (bf16, us): up to 512 a wave with 8 elements a lane (11136 x 512: 14.9; with
-// 16: 15.4), up to 1024 a wave with 16 (16384 x 1024: 30.4; a workgroup of 512
-// threads for two rows: 37), to 2048 two rows of 256 threads (11136 x 2048:
-// 38.4; a wave with 32: 40.9), to 4096 256 threads with 16 (11136 x 3584: 62.6;
-// two rows 65.6, 32 elements 68.4), to 8192 512 threads with 16 (1000 x 6000:
-// 15.2; 256 with 32: 17.2).
 template <class T, class W, int E>
 int bwd_few(const BwdArgs& a, void* dw, void* db, hipStream_t st) {
   const int64_t cols = dw || db ? (a.D + 63) / 64 : 0;
@@ -700,8 +701,23 @@ int bwd_few_typed(const BwdArgs& a, void* dw, void* db, hipStream_t st) {
   return bwd_few<T, W, 32>(a, dw, db, st);
 }
 
+// Threads to a row by its width, each side measured at two widths or more
+// (bf16, us): a vector to a lane up to 512 (fp32 256), so that narrow rows have 8,
+// 16 or 32 lanes of a wave (1048576 x 64: 73.7, a wave to a row 519; 524288 x 128:
+// 72.4 and 262; fp32 524288 x 128: 144 and 234, with two vectors to a lane 147), in
+// workgroups of 1024 (512: 76.8, 76.5 and 183); to 512 a wave with 8 elements a lane
+// (11136 x 512: 14.9; with 16: 15.4), up to 1024 a wave with 16 (16384 x 1024: 30.4;
+// a workgroup of 512 threads for two rows: 37), to 2048 two rows of 256 threads
+// (11136 x 2048: 38.4; a wave with 32: 40.9), to 4096 256 threads with 16 (11136 x
+// 3584: 62.6; two rows 65.6, 32 elements 68.4), to 8192 512 threads with 16 (1000 x
+// 6000: 15.2; 256 with 32: 17.2).
 template <class T, class W>
 int bwd_typed(const BwdArgs& a, int64_t* parts, hipStream_t st) {
+  constexpr int V = Vec<T>::N;
+  if (a.D <= 8 * V) return bwd_go<T, W, 8, V, 1024>(a, parts, st);
+  if (a.D <= 16 * V) return bwd_go<T, W, 16, V, 1024>(a, parts, st);
+  if (a.D <= 32 * V) return bwd_go<T, W, 32, V, 1024>(a, parts, st);
+  if (a.D <= 64 * V) return bwd_go<T, W, 64, V, 512>(a, parts, st);
   if (a.D <= 64 * 8) return bwd_go<T, W, 64, 8, 512>(a, parts, st);
   if (a.D <= 64 * 16) return bwd_go<T, W, 64, 16, 256>(a, parts, st);
   if (a.D <= 256 * 8) return bwd_go<T, W, 256, 8, 512>(a, parts, st);

@@ -356,3 +356,46 @@ def test_binding_refuses_what_the_kernels_cannot_take():
             bad()
     with pytest.raises(sw.SwiGLUError):
         sw.swiglu_layer_norm_fwd(x, w, y=x)
+
+
+# several rows to a wave: widths around each number of lanes, rows that fill a
+# workgroup, a launch and neither
+@pytest.mark.parametrize("t,wt", COMBOS)
+@pytest.mark.parametrize("D", [1, 7, 8, 9, 31, 32, 33, 63, 64, 65, 100, 127, 128, 129, 254, 255, 256, 257])
+@pytest.mark.parametrize("M", [1, 515, 1029, 4111, 40009])
+def test_narrow_rows(M, D, t, wt):
+    x, w, b, dy, res = make(M, D, TYPES[t], TYPES[wt])
+    X, W, B, DY, R = cuda(x, w, b, dy, res)
+    y, mean, rstd = sw.swiglu_layer_norm_fwd(X, W, B, EPS)
+    check_fwd(x, w, b, y, mean, rstd)
+    dx, dw, db = sw.swiglu_layer_norm_bwd(DY, X, W, mean, rstd, dres=R)
+    check_bwd(x, w, mean.cpu(), rstd.cpu(), dy, res, dx, dw, db)
+    again = sw.swiglu_layer_norm_bwd(DY, X, W, mean, rstd, dres=R)
+    assert all(torch.equal(p, q) for p, q in zip((dx, dw, db), again))
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("D", [5, 32, 64, 100, 128, 250])
+def test_narrow_rows_are_alone(D, t):
+    """An infinite or NaN row of a wave leaves its neighbours' bits alone; rows
+    that start at odd elements; nothing beside the outputs is written."""
+    M = 1301
+    x, w, b, dy, _ = make(M, D, TYPES[t], torch.float32)
+    X, W, B, DY = cuda(x, w, b, dy)
+    y, mean, rstd = sw.swiglu_layer_norm_fwd(X, W, B, EPS)
+    dx, _, _ = sw.swiglu_layer_norm_bwd(DY, X, W, mean, rstd)
+    wide = torch.full((M, D + 5), 7.0, dtype=TYPES[t], device="cuda")
+    X2, Y2 = wide.clone()[:, 3:3 + D].copy_(X), wide.clone()
+    bad = [0, 2, 9, 700, M - 1]
+    X2[bad[0], 0], X2[bad[1], D - 1] = float("nan"), float("inf")
+    X2[bad[2]], X2[bad[3], D // 2], X2[bad[4], 0] = float("nan"), -float("inf"), float("nan")
+    good = torch.ones(M, dtype=torch.bool, device="cuda")
+    good[bad] = False
+    y2, m2, r2 = sw.swiglu_layer_norm_fwd(X2, W, B, EPS, y=Y2[:, 3:3 + D])
+    assert torch.equal(y2[good], y[good]) and torch.equal(m2[good], mean[good]) and torch.equal(r2[good], rstd[good])
+    assert y2[bad].isnan().all() and (Y2[:, :3] == 7).all() and (Y2[:, 3 + D:] == 7).all()
+    D2 = wide.clone()
+    dx2, dw2, db2 = sw.swiglu_layer_norm_bwd(DY, X2, W, m2, r2, dx=D2[:, 3:3 + D])
+    assert torch.equal(dx2[good], dx[good]) and dx2[bad].isnan().all()
+    assert (D2[:, :3] == 7).all() and (D2[:, 3 + D:] == 7).all()
+    assert dw2.isnan().all() and torch.isfinite(db2).all()
