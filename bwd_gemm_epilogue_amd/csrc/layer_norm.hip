@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(THREADS) ln_bwd_kernel(const BwdArgs a) {
   // ROWS > 1: [ROWS/2][2][C][G] sums of the columns, then [ROWS/2][2][G] of the tail
   __shared__ float acc_lds[ROWS > 1 ? ROWS / 2 * 2 * (C + 1) * G : 1];
   const int tl = threadIdx.x & (G - 1);
-  int sub = threadIdx.x / G;
+  int sub = ROWS > 1 ? threadIdx.x / G : 0;
   if constexpr (G >= 64) sub = __builtin_amdgcn_readfirstlane(sub);
   const int D = a.D, nvec = D / VEC, tail = nvec * VEC + tl;
   const W* w = (const W*)a.w;
