@@ -671,8 +671,8 @@ int64_t route_slices(int64_t D) { return (D + kRouteSlice - 1) / kRouteSlice; }
 
 // Parts of K: so many that the launch has a workgroup for every compute unit
 // when every slot has its expert, but at least a step of 32 for every wave.  One
-// token, two experts: four parts 29.7 us, one 45.5; two workgroups for every
-// unit 34.1 (more parts to write and read).
+// token, two experts: four parts 28.2 us, one 51.0; two workgroups for every
+// unit 29.6 (more parts to write and read).
 int few_splits(int64_t blocks, int64_t slots, int64_t K) {
   int64_t s = kUnits / (blocks * slots);
   const int64_t most = K / (32 * kWaves);
